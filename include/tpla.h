@@ -29,8 +29,9 @@
  *     is owned by the caller.  The library never frees or retains pointers.
  *   - Every call is asynchronous on `stream` (NULL = legacy default stream)
  *     and performs no host synchronisation, except tpla_get_device_status.
- *   - Inputs are never modified, except the buffer of tpla_hadamard_apply
- *     and the cache of tpla_cache_append / tpla_prefill.
+ *   - Inputs are never modified, except the buffer of tpla_hadamard_apply,
+ *     the cache of tpla_cache_append / tpla_prefill and the caches of
+ *     tpla_kv_append.
  *   - Some kernels after the first of a call (the split-KV merge, the V
  *     up-projection) are launched as programmatic dependents of the kernel
  *     before them in the stream: they start their set-up early and read
@@ -61,7 +62,7 @@ extern "C" {
 /* cudaStream_t without including CUDA headers. */
 typedef struct CUstream_st* tpla_stream_t;
 
-enum tpla_dtype { TPLA_BF16 = 1, TPLA_F32 = 2, TPLA_I32 = 3 };
+enum tpla_dtype { TPLA_BF16 = 1, TPLA_F32 = 2, TPLA_I32 = 3, TPLA_F16 = 4 };
 
 enum tpla_status {
   TPLA_OK = 0,
@@ -382,6 +383,119 @@ TPLA_API int tpla_prefill(const tpla_tensor* q, const tpla_tensor* kv_new, int s
 /* tpla_prefill_workspace_size -- bytes of workspace tpla_prefill needs for
  * queries q ([T, H, 576] bf16) on the current device. */
 TPLA_API int tpla_prefill_workspace_size(const tpla_tensor* q, size_t* bytes);
+
+/*
+ * Attention over UNCOMPRESSED keys and values: the cache that grouped-head
+ * and per-head models keep where MLA keeps its latent rows (the feature
+ * request, "Background / problem", sets the two against each other), and the
+ * form in which MLA's own prompts attend once the latent has been projected
+ * up again (128 + 64 key and 128 value columns a head).
+ *
+ * Common to the three entry points:
+ *   - Caches are k [num_blocks, 64, Hkv, Dk] and v [num_blocks, 64, Hkv, Dv]
+ *     with a page table [B, max_pages] int32 (64-token pages, as in
+ *     tpla_decode_ex), or [B, Lmax, Hkv, D] without one.  Any strides, so
+ *     [num_blocks, Hkv, 64, D] storage is a transposed view; rows start on
+ *     16-byte boundaries and no dimension of more than one entry has stride 0.
+ *   - BF16 or F16 (TPLA_F16); k, v, q of one type.
+ *   - Hq a multiple of Hkv: query head h reads key head h / (Hq / Hkv).
+ *   - Page ids outside [0, num_blocks), lengths and positions outside the
+ *     cache are not read or written: TPLA_ERR_DEVICE_BOUNDS is recorded
+ *     (tpla_get_device_status) and such tokens count as absent.
+ *
+ * tpla_kv_append -- store T new tokens, rotated by their positions.
+ *   k_new     [T, Hkv, Dk], v_new [T, Hkv, Dv]: the caches' type or F32.
+ *             v_new and v_cache both NULL: a cache of one tensor (Hkv = 1 and
+ *             Dk = 576 stores latent rows, already normalised, for
+ *             tpla_decode_ex with their rope columns rotated).
+ *   positions [T] int32, contiguous: the token's index in its request.  -1
+ *             marks a padding row, which is skipped.  No two tokens of a call
+ *             may have the same place.
+ *   requests  [T] int32, contiguous, or NULL: the token's page-table row (or
+ *             request of a contiguous cache); NULL: token t is request t's.
+ *   cos_sin   [table_rows, rot] f32 or NULL (no rotation): row p holds the
+ *             cosines of position p's rot / 2 angles, then their sines.  rot
+ *             is a multiple of 16, rows on 16-byte boundaries.
+ *   rope_offset  first rotated column of k_new, a multiple of 8.
+ *   interleaved  0: column off + j turns with off + rot/2 + j; 1: off + 2j
+ *             turns with off + 2j + 1.  (a, b) -> (a cos - b sin, b cos + a sin),
+ *             f32 arithmetic, rounded once to the cache's type.
+ *   q, q_out  [T, Hq, Dq] or both NULL: queries turned the same way from
+ *             column q_rope_offset on; q F32 or the caches' type, q_out the
+ *             caches' type.  q_out may be q itself; otherwise they must not
+ *             overlap.
+ * A token that cannot be stored (its position, request or page id out of
+ * range, or its position not in the table) leaves the caches and its row of
+ * q_out as they were.  Widths are multiples of 8.
+ * Limits (TPLA_ERR_UNSUPPORTED): B <= 2^20, T <= 2^30, Hkv and Hq <= 4096,
+ * widths <= 4096, pages other than 64 tokens.
+ */
+TPLA_API int tpla_kv_append(const tpla_tensor* k_new, const tpla_tensor* v_new,
+                            const tpla_tensor* positions, const tpla_tensor* requests,
+                            const tpla_tensor* page_table, tpla_tensor* k_cache,
+                            tpla_tensor* v_cache, const tpla_tensor* cos_sin, int rope_offset,
+                            int interleaved, const tpla_tensor* q, tpla_tensor* q_out,
+                            int q_rope_offset, tpla_stream_t stream);
+
+/*
+ * tpla_kv_decode -- attention of one new token per request:
+ *   s_t = scale * (q[b,h] . k_t),  out[b,h] = sum_t softmax(s)_t v_t,
+ *   lse[b,h] = ln sum_t exp(s_t)   over the request's seq_lens[b] tokens.
+ *   q         [B, Hq, Dk];  (Dk, Dv) one of (64, 64), (128, 128), (192, 128).
+ *   seq_lens  [B] int32, contiguous (0 allowed: out = 0, lse = -inf).
+ *   out       [B, Hq, Dv], F32 or q's type, rows on 16-byte boundaries;
+ *   lse       [B, Hq, 1] f32 or NULL.
+ *   scale     any finite value.
+ *   workspace tpla_kv_decode_workspace_size bytes, 16-byte aligned, or NULL
+ *             (cudaMallocAsync / cudaFreeAsync on `stream`).  Calls that may
+ *             run at the same time need workspaces of their own.
+ * The cache is read once, split evenly over the GPU's SMs whatever the
+ * lengths, and the pieces are joined by the log-sum-exp rule.  What stands
+ * behind a request's last token in its page is never used (it may be NaN).
+ * Weights are rounded to the 16-bit type for the product with v; sums and
+ * the log-sum-exp are f32.
+ * Limits (TPLA_ERR_UNSUPPORTED): other widths, B <= 2^20, Hq <= 4096,
+ * B * Hq <= 2^30, tokens of a request <= 2^30, pages other than 64 tokens, no
+ * sm_100 GPU.
+ */
+TPLA_API int tpla_kv_decode_workspace_size(const tpla_tensor* q, const tpla_tensor* k_cache,
+                                           const tpla_tensor* v_cache,
+                                           const tpla_tensor* page_table, size_t* bytes);
+TPLA_API int tpla_kv_decode(const tpla_tensor* q, const tpla_tensor* k_cache,
+                            const tpla_tensor* v_cache, const tpla_tensor* seq_lens,
+                            const tpla_tensor* page_table, float scale, tpla_tensor* out,
+                            tpla_tensor* lse, void* workspace, size_t workspace_bytes,
+                            tpla_stream_t stream);
+
+/*
+ * tpla_kv_prefill -- attention of packed prompts (any number of tokens each).
+ * Request b has T_b = cu_q[b+1] - cu_q[b] query rows, from row cu_q[b] on, and
+ * L_b keys; its token i attends over its keys j < L_b, and with causal = 1
+ * over j < L_b - T_b + i + 1 (the last token sees every key).  A token that
+ * sees no key gets out = 0 and lse = -inf.  Rows of out and lse that belong
+ * to no request are left as they were.
+ *   q      [T, Hq, Dk], widths as in tpla_kv_decode.
+ *   k, v   packed: [Tk, Hkv, D], request b's rows from cu_k[b] on (cu_k NULL:
+ *          cu_q); page_table and seq_lens NULL.
+ *          paged: the caches, with page_table and seq_lens [B] int32 (L_b:
+ *          cached tokens and the prompt's own, stored before this call, for
+ *          instance by tpla_kv_append); cu_k NULL.
+ *   cu_q, cu_k  [B + 1] int32, contiguous, rising; entries outside the
+ *          tensors are clipped and recorded as TPLA_ERR_DEVICE_BOUNDS.
+ *   out    [T, Hq, Dv], F32 or q's type, rows on 16-byte boundaries; lse
+ *          [T, Hq, 1] f32 or NULL; scale, workspace as in tpla_kv_decode.
+ * Keys and values of a request must be finite (a later token's infinity or
+ * NaN in v reaches earlier rows of its 128-key tile through a weight of 0);
+ * what stands behind its last key is never used.
+ * Limits (TPLA_ERR_UNSUPPORTED): B <= 2^20, T and Tk <= 2^30, Hq <= 4096.
+ */
+TPLA_API int tpla_kv_prefill_workspace_size(const tpla_tensor* q, const tpla_tensor* k,
+                                            const tpla_tensor* cu_q, size_t* bytes);
+TPLA_API int tpla_kv_prefill(const tpla_tensor* q, const tpla_tensor* k, const tpla_tensor* v,
+                             const tpla_tensor* cu_q, const tpla_tensor* cu_k,
+                             const tpla_tensor* seq_lens, const tpla_tensor* page_table,
+                             int causal, float scale, tpla_tensor* out, tpla_tensor* lse,
+                             void* workspace, size_t workspace_bytes, tpla_stream_t stream);
 
 /* Human-readable name of a tpla_status code (static string). */
 TPLA_API const char* tpla_error_string(int status);

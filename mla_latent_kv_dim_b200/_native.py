@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -17,7 +18,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libtpla.so")
 
-TPLA_BF16, TPLA_F32, TPLA_I32 = 1, 2, 3
+TPLA_BF16, TPLA_F32, TPLA_I32, TPLA_F16 = 1, 2, 3, 4
 ROPE_MODES = {"replicate": 0, "split": 1}
 KERNELS = {"auto": 0, "generic": 1, "sm100": 2}
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported", -3: "CUDA error",
@@ -86,7 +87,16 @@ def lib() -> ctypes.CDLL:
                                        ctypes.c_float, ctypes.c_float, T, T, ctypes.c_void_p,
                                        ctypes.c_size_t, ctypes.c_void_p]
             L.tpla_prefill_workspace_size.argtypes = [T, _P(ctypes.c_size_t)]
-            for f in ("tpla_decode_ex", "tpla_decode", "tpla_decode_workspace_size",
+            # the kv_* entry points take descriptor addresses (see _descs)
+            V, Z, I, F = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
+            L.tpla_kv_append.argtypes = [V] * 8 + [I, I, V, V, I, V]
+            L.tpla_kv_decode.argtypes = [V] * 5 + [F, V, V, V, Z, V]
+            L.tpla_kv_decode_workspace_size.argtypes = [V] * 4 + [_P(Z)]
+            L.tpla_kv_prefill.argtypes = [V] * 7 + [I, F, V, V, V, Z, V]
+            L.tpla_kv_prefill_workspace_size.argtypes = [V] * 3 + [_P(Z)]
+            for f in ("tpla_kv_append", "tpla_kv_decode", "tpla_kv_decode_workspace_size",
+                      "tpla_kv_prefill", "tpla_kv_prefill_workspace_size",
+                      "tpla_decode_ex", "tpla_decode", "tpla_decode_workspace_size",
                       "tpla_lse_merge", "tpla_hadamard_apply", "tpla_vup_combine",
                       "tpla_last_cuda_error", "tpla_get_device_status", "tpla_version",
                       "tpla_selftest_wait_timeout", "tpla_latent_covariance",
@@ -103,7 +113,8 @@ def _check(fn: str, rc: int) -> None:
         raise TplaError(fn, rc, lib().tpla_last_cuda_error() if rc == -3 else 0)
 
 
-_DT = {torch.bfloat16: TPLA_BF16, torch.float32: TPLA_F32, torch.int32: TPLA_I32}
+_DT = {torch.bfloat16: TPLA_BF16, torch.float32: TPLA_F32, torch.int32: TPLA_I32,
+       torch.float16: TPLA_F16}
 
 
 def desc(t: torch.Tensor | None):
@@ -333,6 +344,123 @@ def prefill(q, kv_new, start, page_row, kv_cache, norm_groups=1, hadamard=False,
         _ref(desc(out)), _ref(desc(lse)), workspace.data_ptr() if need else None,
         workspace.numel() * workspace.element_size() if need else 0, _stream(stream))
     _check("tpla_prefill", rc)
+    return out, lse
+
+
+# ---------------------------------------------------------------- uncompressed keys and values
+_PACKED = struct.Struct("Pii8q")  # one tpla_tensor
+_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
+
+
+def _descs(*tensors):
+    """Descriptors of the tensors in one buffer (kept by the caller for the
+    call) and their addresses (None for None): a decode step makes these
+    calls per layer, so their host time counts."""
+    size = _PACKED.size
+    buf = ctypes.create_string_buffer(size * len(tensors))
+    base = ctypes.addressof(buf)
+    at = []
+    for i, t in enumerate(tensors):
+        if t is None:
+            at.append(None)
+            continue
+        if t.dtype not in _DT:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        n = t.dim()
+        if n > 4:
+            raise ValueError("at most 4 dimensions")
+        pad = _PAD[n]
+        _PACKED.pack_into(buf, i * size, t.data_ptr(), _DT[t.dtype], n, *t.shape, *pad,
+                          *t.stride(), *pad)
+        at.append(base + i * size)
+    return buf, at
+
+
+def _scratch(workspace, need, device):
+    """A workspace of at least ``need`` bytes (the caller's where it is large
+    enough): (the tensor to keep, address, bytes)."""
+    if not need:
+        return None, None, 0
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def kv_append(k_new, v_new, positions, page_table, k_cache, v_cache, *, requests=None,
+              cos_sin=None, rope_offset=0, interleaved=False, q=None, q_out=None,
+              q_rope_offset=None, stream=None):
+    """Store new tokens' keys and values ([T, Hkv, Dk], [T, Hkv, Dv]) at
+    ``positions`` [T] of their requests, rotating the keys (and ``q``
+    [T, Hq, Dq]) by the table ``cos_sin`` [positions, rot] on the way
+    (tpla_kv_append).  ``requests`` [T] names each token's page-table row;
+    without it token t is request t's.  ``v_new`` and ``v_cache`` may both be
+    None (a cache of one tensor, such as latent rows with their rope columns).
+    In place on the caches; returns the rotated queries (``q_out``, which may
+    be ``q``), or None without ``q``."""
+    _on_current_device(k_new, v_new, positions, page_table, k_cache, v_cache, requests, cos_sin,
+                       q, q_out)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=k_cache.dtype, device=q.device)
+    if q_rope_offset is None:
+        q_rope_offset = rope_offset
+    buf, d = _descs(k_new, v_new, positions, requests, page_table, k_cache, v_cache, cos_sin, q,
+                    q_out)
+    rc = lib().tpla_kv_append(*d[:8], int(rope_offset), 1 if interleaved else 0, d[8], d[9],
+                              int(q_rope_offset), _stream(stream))
+    _check("tpla_kv_append", rc)
+    return q_out
+
+
+def kv_decode(q, k_cache, v_cache, seq_lens, page_table, scale=None, out=None, lse=None, *,
+              workspace=None, out_dtype=torch.float32, want_lse=True, stream=None):
+    """Attention of one new token per request (``q`` [B, Hq, Dk]) over the
+    uncompressed cache ([num_blocks, 64, Hkv, D] with a page table, or
+    [B, Lmax, Hkv, D] with None), Hq / Hkv query heads to a key head
+    (tpla_kv_decode).  Returns (out [B, Hq, Dv], lse [B, Hq, 1])."""
+    if scale is None:
+        raise ValueError("scale is required")
+    _on_current_device(q, k_cache, v_cache, seq_lens, page_table, out, lse, workspace)
+    if out is None:
+        out = torch.empty((q.shape[0], q.shape[1], v_cache.shape[-1]), dtype=out_dtype,
+                          device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((q.shape[0], q.shape[1], 1), dtype=torch.float32, device=q.device)
+    buf, d = _descs(q, k_cache, v_cache, seq_lens, page_table, out, lse)
+    n = ctypes.c_size_t(0)
+    _check("tpla_kv_decode_workspace_size",
+           lib().tpla_kv_decode_workspace_size(d[0], d[1], d[2], d[4], ctypes.byref(n)))
+    workspace, ws, size = _scratch(workspace, n.value, q.device)
+    rc = lib().tpla_kv_decode(*d[:5], scale, d[5], d[6], ws, size, _stream(stream))
+    _check("tpla_kv_decode", rc)
+    return out, lse
+
+
+def kv_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, seq_lens=None, page_table=None,
+               scale=None, causal=True, out=None, lse=None, workspace=None,
+               out_dtype=torch.float32, want_lse=True, stream=None):
+    """Attention of packed prompts: request b's tokens are rows
+    ``cu_seqlens_q[b]`` .. ``cu_seqlens_q[b + 1] - 1`` of ``q`` [T, Hq, Dk]
+    (tpla_kv_prefill).  Keys and values are packed too ([Tk, Hkv, D], rows by
+    ``cu_seqlens_k``, by default those of q) or, with ``page_table`` and
+    ``seq_lens``, in the paged cache [num_blocks, 64, Hkv, D], where the
+    prompt's own rows have been stored already.  ``causal`` lines the last
+    token up with the last key.  Returns (out [T, Hq, Dv], lse [T, Hq, 1])."""
+    if scale is None:
+        raise ValueError("scale is required")
+    _on_current_device(q, k, v, cu_seqlens_q, cu_seqlens_k, seq_lens, page_table, out, lse,
+                       workspace)
+    if out is None:
+        out = torch.empty((q.shape[0], q.shape[1], v.shape[-1]), dtype=out_dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((q.shape[0], q.shape[1], 1), dtype=torch.float32, device=q.device)
+    buf, d = _descs(q, k, v, cu_seqlens_q, cu_seqlens_k, seq_lens, page_table, out, lse)
+    n = ctypes.c_size_t(0)
+    _check("tpla_kv_prefill_workspace_size",
+           lib().tpla_kv_prefill_workspace_size(d[0], d[1], d[3], ctypes.byref(n)))
+    workspace, ws, size = _scratch(workspace, n.value, q.device)
+    rc = lib().tpla_kv_prefill(*d[:7], 1 if causal else 0, scale, d[7], d[8], ws, size,
+                               _stream(stream))
+    _check("tpla_kv_prefill", rc)
     return out, lse
 
 

@@ -14,6 +14,8 @@ namespace {
 thread_local int t_last_cuda_error = 0;
 std::atomic<int64_t> g_launches{0};
 
+}  // namespace
+
 int cuda_fail(cudaError_t e) {
   t_last_cuda_error = (int)e;
   return TPLA_ERR_CUDA;
@@ -21,11 +23,15 @@ int cuda_fail(cudaError_t e) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+namespace {
+
 // Launch-geometry limits the entry points check before any launch.
 constexpr int kMaxSplits = 65535;                     // a grid dimension of the generic kernel
 constexpr int64_t kMaxRequestHeads = 1LL << 30;       // B * H: merge blocks, 32-bit grid
 constexpr int64_t kMaxRequestSplits = 1LL << 24;      // B * num_splits: 2x that many slots
 constexpr int64_t kMaxGenericRequestShards = 65535;   // B * shards: the generic grid's z
+
+}  // namespace
 
 bool check_tensor(const tpla_tensor* t, int dtype, int ndim) {
   if (!t || t->dtype != dtype || t->ndim != ndim) return false;
@@ -45,6 +51,8 @@ int current_device() {
   cudaGetDevice(&dev);
   return dev;
 }
+
+namespace {
 
 // Flatten and validate a decode call.
 int build_problem(const tpla_tensor* q, const tpla_tensor* kv, const tpla_tensor* seq,
@@ -594,7 +602,16 @@ int tpla_get_device_status(tpla_stream_t stream, int* status) {
   if (e != cudaSuccess) return cuda_fail(e);
   e = status_read_clear_append(&d);
   if (e != cudaSuccess) return cuda_fail(e);
-  *status = a != 0 ? a : (b != 0 ? b : (c != 0 ? c : d));
+  int kv[3] = {0, 0, 0};
+  e = status_read_clear_kv_append(&kv[0]);
+  if (e != cudaSuccess) return cuda_fail(e);
+  e = status_read_clear_kv_decode(&kv[1]);
+  if (e != cudaSuccess) return cuda_fail(e);
+  e = status_read_clear_kv_prefill(&kv[2]);
+  if (e != cudaSuccess) return cuda_fail(e);
+  *status = 0;
+  for (int s : {a, b, c, d, kv[0], kv[1], kv[2]})
+    if (*status == 0) *status = s;
   return TPLA_OK;
 }
 

@@ -102,6 +102,84 @@ cudaError_t launch_cache_append(const void* kv_new, int in_bf16, int64_t n_sb, c
                                 int64_t c_s1, int B, int groups, int hadamard, float eps,
                                 cudaStream_t stream);
 
+// ---------------------------------------------------------------- uncompressed keys and values
+// One validated tpla_kv_append call.  A piece is one thread's work in a row:
+// 8 plain columns, or 8 interleaved pair columns, or 8 + 8 columns of pairs in
+// halves.
+struct KvAppendProblem {
+  const void *k, *v, *q;        // [T, Hkv, Dk], [T, Hkv, Dv] or null, [T, Hq, Dq] or null
+  int64_t k_st, k_sh, v_st, v_sh, q_st, q_sh;
+  int kv_f32, q_f32;            // f32 sources (else the cache's type)
+  void *k_cache, *v_cache, *q_out;
+  int64_t kc_s0, kc_s1, kc_s2, vc_s0, vc_s1, vc_s2, qo_st, qo_sh;
+  int64_t num_blocks, cap_rows; // cap_rows: tokens one request's cache can hold
+  const int* positions;         // [T]
+  const int* requests;          // [T] or null: row t belongs to request t
+  const int* page_table;        // [B, max_pages] or null (contiguous)
+  int64_t pt_sb;
+  int B;
+  const float* cos_sin;         // [table_rows, rot] or null
+  int64_t cs_s;
+  int64_t table_rows;
+  int rot, k_off, q_off, interleaved;
+  int T, Hkv, Hq, k_pieces, v_pieces, q_pieces;
+  int f16;
+};
+cudaError_t launch_kv_append(const KvAppendProblem& p, cudaStream_t stream);
+
+// Keys and values as the attention kernels read them: paged
+// [num_blocks, 64, Hkv, D], contiguous [B, rows, Hkv, D] (page_table null).
+struct KvSource {
+  const void *k, *v;
+  int64_t k_s0, k_s1, k_s2, v_s0, v_s1, v_s2;  // page (or request), row, head strides
+  int64_t num_blocks;           // pages, or requests of a contiguous cache
+  int64_t cap_rows;             // tokens one request can hold
+  const int* seq_lens;          // [B]
+  const int* page_table;        // [B, max_pages] or null
+  int64_t pt_sb;
+  int Hkv, Dk, Dv, f16;
+};
+
+struct KvDecodeProblem {
+  KvSource kv;
+  const void* q;                // [B, Hq, Dk]
+  int64_t q_sb, q_sh;
+  int B, Hq;
+  float scale;
+  void* out;                    // [B, Hq, Dv]
+  int out_dtype;
+  int64_t o_sb, o_sh;
+  float* lse;                   // [B, Hq, 1] or null
+  int64_t l_sb, l_sh;
+};
+bool kv_head_dims_supported(int Dk, int Dv);
+size_t kv_decode_workspace_bytes(const KvDecodeProblem& p, int device);
+cudaError_t launch_kv_decode(const KvDecodeProblem& p, void* ws, cudaStream_t stream);
+
+// kv.page_table null: packed keys and values, request b's rows start at
+// cu_k[b] of [Tk, Hkv, D] (k_s1, v_s1 are the row strides, cap_rows is Tk).
+struct KvPrefillProblem {
+  KvSource kv;
+  const void* q;                // [T, Hq, Dk]
+  int64_t q_st, q_sh;
+  const int *cu_q, *cu_k;       // [B + 1]; cu_k null with a paged cache
+  int B, T, Hq, causal;
+  float scale;
+  void* out;                    // [T, Hq, Dv]
+  int out_dtype;
+  int64_t o_st, o_sh;
+  float* lse;                   // [T, Hq, 1] or null
+  int64_t l_st, l_sh;
+};
+size_t kv_prefill_workspace_bytes(const KvPrefillProblem& p);
+cudaError_t launch_kv_prefill(const KvPrefillProblem& p, void* ws, cudaStream_t stream);
+
+// ---------------------------------------------------------------- argument checks (api.cu)
+int cuda_fail(cudaError_t e);  // remembers e for tpla_last_cuda_error; TPLA_ERR_CUDA
+bool aligned16(const void* p);
+bool check_tensor(const tpla_tensor* t, int dtype, int ndim);
+int current_device();
+
 // ---------------------------------------------------------------- launch counter
 // Called once per kernel launch by every launcher.
 void count_launch(int n = 1);
@@ -113,6 +191,9 @@ cudaError_t status_read_clear_generic(int* code);
 cudaError_t status_read_clear_sm100(int* code);
 cudaError_t status_read_clear_vup(int* code);
 cudaError_t status_read_clear_append(int* code);
+cudaError_t status_read_clear_kv_append(int* code);
+cudaError_t status_read_clear_kv_decode(int* code);
+cudaError_t status_read_clear_kv_prefill(int* code);
 cudaError_t launch_wait_timeout_selftest(long long cycles, cudaStream_t stream);
 
 }  // namespace tpla

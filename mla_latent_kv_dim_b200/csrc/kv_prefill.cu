@@ -1,0 +1,779 @@
+// Causal (or full) attention of packed prompts over uncompressed keys and
+// values, with grouped heads, on the 5th-generation tensor cores:
+//   s_ij = scale q_i . k_j,  j < limit_i;   out_i = sum_j softmax(s_i)_j v_j,
+//   lse_i = ln sum_j exp(s_ij);   limit_i = L or, causal, L - T + i + 1
+// for a request's T new tokens against its L keys (packed rows, or the paged
+// cache with the prompt's own keys already in it).
+//
+// The two matrix products bound it (2 (Dk + Dv) flops a pair and head), and
+// beside them the exponentials: one per score on a unit that gives 16 a cycle
+// against the 128 x 128 x 16 product's 64 cycles.  So:
+//  * a tile is 128 rows: tpt = 128 / g tokens times the g query heads of one
+//    key head (row = token * g + head), so that grouped heads share every
+//    key and value tile and few tokens still fill the rows;
+//  * a work item is two such tiles A and B of consecutive tokens.  One thread
+//    issues S = Q K^T (N = 128 keys) and O += P V for both in turn; while the
+//    tensor core works on one, the other's softmax warpgroup turns its S into
+//    P.  S and P share TMEM columns (P goes over S as 16-bit pairs, the A
+//    operand from TMEM), O stays in TMEM: 2 x (128 + Dv) of the 512 columns;
+//  * a thread owns a row: no exchange for the row maximum.  O is rescaled
+//    only when the maximum has grown by more than 2^8;
+//  * K and V tiles go through one ring of 16 KB stages (128 keys x 64 columns,
+//    128-byte swizzle, K-major for Q K^T and MN-major for P V);
+//  * items are handed out longest first (a small kernel sorts them; one
+//    request needs no sorting), so the last ones are short.
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "internal.h"
+#include "kv_map.h"
+#include "kv_ptx.cuh"
+
+namespace tpla {
+namespace {
+
+using namespace kvx;
+
+__device__ int g_kv_prefill_status;
+
+constexpr int kTile = 128;     // rows of a query tile, keys of a key tile
+constexpr int kStage = 16384;  // 128 keys x 64 columns
+constexpr int kThreads = 384;
+constexpr int kWarpMma = 0, kWarpProd = 1, kWarpSm0 = 4;  // 4-7: tile A, 8-11: tile B
+constexpr int kMaxRing = 12;
+constexpr int kFlagRing = 8;   // key tiles whose page flags are kept (ring / stages of a tile < 8)
+constexpr int kSmemBytes = 232448;
+constexpr int kMiscBytes = 2048;
+constexpr int kBuckets = 2048;  // of the items' lengths
+constexpr uint32_t kColS = 0, kColO = 256;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+
+struct Entry {  // two query tiles of one request
+  int t0;       // first token within the request
+  int q0, qlen; // the request's rows of q
+  int k0;       // packed: its first row of k
+  int kvlen;    // its keys
+  int b, pad0, pad1;
+};
+
+struct Params {
+  const int *cu_q, *cu_k, *seq_lens, *page_table;
+  int64_t pt_sb;
+  int num_blocks;
+  int cap_rows;
+  int B, T, Hkv, g, gg, groups, tpt;  // gg heads of a row group, tpt tokens of a tile
+  int causal;
+  float scale_log2;
+  const int* count;      // entries of the list, or null: one request, no list
+  const Entry* list;
+  void* out;
+  int out_dtype;
+  int64_t o_st, o_sh;
+  float* lse;
+  int64_t l_st, l_sh;
+};
+
+struct Item {
+  Entry e;
+  int hk, rg;
+  int n[2];  // key tiles of the two query tiles
+  int nmax;
+};
+
+__device__ __forceinline__ void bounds() {
+  atomicCAS(&g_kv_prefill_status, 0, TPLA_ERR_DEVICE_BOUNDS);
+}
+
+// A request's rows of q and keys, clipped to the tensors.
+__device__ __forceinline__ void request(const Params& p, int b, Entry& e) {
+  const int a = p.cu_q[b], z = p.cu_q[b + 1];
+  const int lo = max(0, min(a, p.T)), hi = max(lo, min(z, p.T));
+  bool bad = lo != a || hi != z;
+  e.b = b;
+  e.q0 = lo;
+  e.qlen = hi - lo;
+  if (p.page_table) {
+    const int n = p.seq_lens[b];
+    e.k0 = 0;
+    e.kvlen = max(0, min(n, p.cap_rows));
+    bad |= e.kvlen != n;
+  } else {
+    const int ka = p.cu_k[b], kz = p.cu_k[b + 1];
+    const int kl = max(0, min(ka, p.cap_rows)), kh = max(kl, min(kz, p.cap_rows));
+    bad |= kl != ka || kh != kz;
+    e.k0 = kl;
+    e.kvlen = kh - kl;
+  }
+  if (bad) bounds();
+}
+
+// Keys that token `tok` of the request sees.
+__device__ __forceinline__ int limit_of(const Params& p, const Entry& e, int tok) {
+  if (!p.causal) return e.kvlen;
+  return max(0, min(e.kvlen, e.kvlen - e.qlen + tok + 1));
+}
+
+__device__ __forceinline__ int item_count(const Params& p) {
+  int n;
+  if (p.count) {
+    n = *p.count;
+  } else {
+    Entry e;
+    request(p, 0, e);
+    n = (e.qlen + 2 * p.tpt - 1) / (2 * p.tpt);
+  }
+  return n * p.Hkv * p.groups;
+}
+
+__device__ __forceinline__ void get_item(const Params& p, int idx, int total, Item& it) {
+  const int heads = p.Hkv * p.groups;
+  const int x = idx / heads, h = idx - x * heads;
+  it.hk = h / p.groups;
+  it.rg = h - it.hk * p.groups;
+  if (p.count) {
+    const int4* s = reinterpret_cast<const int4*>(p.list + x);
+    int4* d = reinterpret_cast<int4*>(&it.e);
+    d[0] = s[0];
+    d[1] = s[1];
+  } else {  // longest first: the last tokens of a causal prompt see the most keys
+    request(p, 0, it.e);
+    it.e.t0 = (total / heads - 1 - x) * 2 * p.tpt;
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int a = it.e.t0 + t * p.tpt, z = min(a + p.tpt, it.e.qlen);
+    it.n[t] = z > a ? (limit_of(p, it.e, z - 1) + kTile - 1) / kTile : 0;
+  }
+  it.nmax = max(it.n[0], it.n[1]);
+}
+
+template <typename T, int DK, int DV>
+struct Cfg {
+  static constexpr int kNK = DK / 64, kNV = DV / 64;  // 64-column chunks
+  static constexpr int kSPT = kNK + kNV;              // ring stages of a key tile
+  static constexpr int kQ = 2 * kNK * kStage;         // both query tiles
+  static constexpr int kRing0 = (kSmemBytes - 1024 - kMiscBytes - kQ) / kStage;
+  static constexpr int kRing = kRing0 < kMaxRing ? kRing0 : kMaxRing;
+  static constexpr int kSmem = 1024 + kQ + kRing * kStage + kMiscBytes;
+  static_assert(kSmem <= kSmemBytes && kRing > kSPT, "shared memory");
+  static_assert((kRing + kSPT - 1) / kSPT + 1 < kFlagRing, "page flags");
+  static constexpr uint32_t idesc(int n, bool b_mn) {
+    return (1u << 4) | ((uint32_t)T::kFormat << 7) | ((uint32_t)T::kFormat << 10) |
+           ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+  }
+};
+
+struct Misc {
+  unsigned long long full[kMaxRing], empty[kMaxRing];
+  unsigned long long q_full, q_empty, s_full[2], p_full[2], pv_done[2];
+  int flags[kFlagRing];
+  uint32_t tmem;
+  int abort_flag;
+};
+static_assert(sizeof(Misc) <= kMiscBytes, "misc shared memory");
+
+template <typename T, int DK, int DV>
+__device__ void producer(const Params& p, const CUtensorMap* qm, const CUtensorMap* km,
+                         const CUtensorMap* vm, uint32_t sbase, Misc& ms) {
+  using C = Cfg<T, DK, DV>;
+  const int lane = threadIdx.x & 31;
+  const uint32_t ring = sbase + C::kQ;
+  volatile int* abort_flag = &ms.abort_flag;
+  const int total = item_count(p);
+  uint32_t n = 0, qloads = 0, tile = 0;
+  for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
+    Item it;
+    get_item(p, idx, total, it);
+    if (it.nmax == 0) continue;
+    int ok = 1;
+    if (lane == 0 && qloads > 0)
+      ok = wait_bar(smem_addr(&ms.q_empty), (qloads - 1) & 1, abort_flag, &g_kv_prefill_status);
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+    ++qloads;
+    const uint32_t qf = smem_addr(&ms.q_full);
+    if (lane == 0) {
+      const int tiles = (it.n[0] > 0) + (it.n[1] > 0);
+      mbar_arrive_expect_tx(qf, tiles * C::kNK * p.gg * p.tpt * 128);
+    }
+    __syncwarp();
+    if (lane < 2 * C::kNK) {
+      const int t = lane / C::kNK, c = lane - t * C::kNK;
+      if (it.n[t] > 0)
+        tma_load_5d(sbase + lane * kStage, qm, 0, it.rg * p.gg, it.e.q0 + it.e.t0 + t * p.tpt, c,
+                    it.hk, qf);
+    }
+    int win = 0;  // lane i: page id 32 w + i
+    for (int j = 0; j < it.nmax; ++j, ++tile) {
+      int pg[2] = {0, 0}, row[2] = {it.e.k0 + kTile * j, it.e.k0 + kTile * j + 64};
+      if (p.page_table) {
+        const int pages = (it.e.kvlen + 63) >> 6;
+        if ((j & 15) == 0) {
+          const int i = 2 * j + lane;
+          win = i < pages ? p.page_table[(int64_t)it.e.b * p.pt_sb + i] : -2;
+        }
+        int flags = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int id = __shfl_sync(0xffffffffu, win, (2 * j + h) & 31);
+          const bool good = id >= 0 && id < p.num_blocks;
+          if (id != -2 || 2 * j + h < pages) flags |= good ? 0 : 1 << h;
+          pg[h] = good ? id : max(p.num_blocks, 1);  // past the last page: reads as zeros
+          row[h] = 0;
+        }
+        if (lane == 0) {
+          if (flags) bounds();
+          ms.flags[tile % kFlagRing] = flags;
+        }
+      }
+      for (int st = 0; st < C::kSPT; ++st, ++n) {
+        const uint32_t slot = n % C::kRing;
+        ok = 1;
+        if (lane == 0 && n >= C::kRing)
+          ok = wait_bar(smem_addr(&ms.empty[slot]), ((n / C::kRing) - 1) & 1, abort_flag,
+                        &g_kv_prefill_status);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+        const uint32_t full = smem_addr(&ms.full[slot]);
+        if (lane == 0) mbar_arrive_expect_tx(full, kStage);
+        __syncwarp();
+        if (lane < 2) {
+          const int c = st < C::kNK ? st : st - C::kNK;
+          tma_load_5d(ring + slot * kStage + lane * (kStage / 2), st < C::kNK ? km : vm, 0,
+                      lane ? row[1] : row[0], c, it.hk, lane ? pg[1] : pg[0], full);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int DK, int DV>
+__device__ void mma_issuer(const Params& p, uint32_t sbase, uint32_t tmem, Misc& ms) {
+  using C = Cfg<T, DK, DV>;
+  volatile int* abort_flag = &ms.abort_flag;
+  const uint32_t ring = sbase + C::kQ;
+  const uint64_t dQ = sw128_desc(sbase, 16, 1024), dK = sw128_desc(ring, 16, 1024);
+  // V, MN-major: rows are keys, 64 columns to a 128-byte row; two chunks in
+  // consecutive stages are one operand whose column groups lie a stage apart
+  const uint64_t dV = sw128_desc(ring, kStage, 1024);
+  const uint32_t q_lo = (uint32_t)dQ, k_lo = (uint32_t)dK, kk_hi = (uint32_t)(dK >> 32);
+  const uint32_t v_lo = (uint32_t)dV, v_hi = (uint32_t)(dV >> 32);
+  constexpr uint32_t kS = kStage >> 4;
+  const int total = item_count(p);
+  uint32_t base = 0, qloads = 0, cnt[2] = {0, 0};
+  auto wait = [&](unsigned long long& bar, uint32_t parity) {
+    return wait_bar(smem_addr(&bar), parity, abort_flag, &g_kv_prefill_status);
+  };
+  auto wait_stages = [&](uint32_t s, int k) {
+    for (int i = 0; i < k; ++i)
+      if (!wait(ms.full[(s + i) % C::kRing], ((s + i) / C::kRing) & 1)) return false;
+    return true;
+  };
+  auto release = [&](uint32_t s, int k) {
+    for (int i = 0; i < k; ++i) commit(smem_addr(&ms.empty[(s + i) % C::kRing]));
+  };
+  for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
+    Item it;
+    get_item(p, idx, total, it);
+    if (it.nmax == 0) continue;
+    auto qk = [&](int t, uint32_t s) {
+#pragma unroll
+      for (int c = 0; c < C::kNK; ++c) {
+        const uint32_t a = q_lo + (uint32_t)(t * C::kNK + c) * kS;
+        const uint32_t b = k_lo + ((s + c) % C::kRing) * kS;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss(tmem + kColS + kTile * t, a + 2 * k, kk_hi, b + 2 * k, kk_hi,
+                 C::idesc(128, false), (c | k) != 0);
+      }
+      commit(smem_addr(&ms.s_full[t]));
+    };
+    if (!wait(ms.q_full, qloads & 1)) return;
+    ++qloads;
+    if (!wait_stages(base, C::kNK)) return;
+    tc_fence_after();
+    for (int t = 0; t < 2; ++t)
+      if (it.n[t] > 0) qk(t, base);
+    release(base, C::kNK);
+    if (it.nmax == 1) commit(smem_addr(&ms.q_empty));
+    for (int j = 0; j < it.nmax; ++j) {
+      const uint32_t s = base + (uint32_t)j * C::kSPT, sv = s + C::kNK, sn = s + C::kSPT;
+      for (int t = 0; t < 2; ++t) {
+        if (j >= it.n[t]) continue;
+        const bool first = t == 0 || j >= it.n[0], last = t == 1 || j >= it.n[1];
+        if (!wait(ms.p_full[t], cnt[t] & 1)) return;
+        ++cnt[t];
+        if (first && !wait_stages(sv, C::kNV)) return;
+        tc_fence_after();
+        const uint32_t pa = tmem + kColS + kTile * t;
+        const uint32_t dO = tmem + kColO + kTile * t;
+        const uint32_t slot = sv % C::kRing;
+        if (C::kNV == 1 || slot + 1 < C::kRing) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ts(dO, pa + 8 * k, v_lo + slot * kS + 128 * k, v_hi, C::idesc(DV, true),
+                   (j | k) != 0);
+        } else {  // the chunks lie at the ring's end and its beginning
+#pragma unroll
+          for (int c = 0; c < C::kNV; ++c)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_ts(dO + 64 * c, pa + 8 * k, v_lo + ((sv + c) % C::kRing) * kS + 128 * k, v_hi,
+                     C::idesc(64, true), (j | k) != 0);
+        }
+        commit(smem_addr(&ms.pv_done[t]));
+        if (last) release(sv, C::kNV);
+        if (j + 1 < it.n[t]) {
+          const bool nfirst = t == 0 || j + 1 >= it.n[0], nlast = t == 1 || j + 1 >= it.n[1];
+          if (nfirst && !wait_stages(sn, C::kNK)) return;
+          tc_fence_after();
+          qk(t, sn);
+          if (nlast) {
+            release(sn, C::kNK);
+            if (j + 2 == it.nmax) commit(smem_addr(&ms.q_empty));
+          }
+        }
+      }
+    }
+    base += (uint32_t)it.nmax * C::kSPT;
+  }
+}
+
+template <typename T, int DK, int DV>
+__device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, Misc& ms) {
+  using C = Cfg<T, DK, DV>;
+  volatile int* abort_flag = &ms.abort_flag;
+  const int w = (int)(threadIdx.x >> 5) & 3;
+  const int row = 32 * w + (int)(threadIdx.x & 31);  // this thread's row and TMEM lane
+  const uint32_t lane_base = (uint32_t)(32 * w) << 16;
+  const uint32_t tS = tmem + lane_base + kColS + kTile * t;
+  const uint32_t tO = tmem + lane_base + kColO + kTile * t;
+  const uint32_t ring = sbase + C::kQ;
+  const int total = item_count(p);
+  const int my_tok = row / p.gg, my_head = row - my_tok * p.gg;
+  uint32_t cnt = 0, tiles = 0;
+  auto wait = [&](unsigned long long& bar, uint32_t parity) {
+    const bool ok = wait_bar(smem_addr(&bar), parity, abort_flag, &g_kv_prefill_status);
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
+  for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
+    Item it;
+    get_item(p, idx, total, it);
+    const int tok = it.e.t0 + t * p.tpt + my_tok;
+    const int head = it.rg * p.gg + my_head;
+    const bool live = my_tok < p.tpt && tok < it.e.qlen && head < p.g;
+    // rows past the tile's tokens or the request's are computed and not stored
+    const int limit = live ? limit_of(p, it.e, tok) : it.e.kvlen;
+    const int n = it.n[t];
+    float m = -INFINITY, l = 0.f, lx = 0.f;  // maximum; sums of the 16-bit and the f32 weights
+    for (int j = 0; j < n; ++j, ++cnt) {
+      if (!wait(ms.s_full[t], cnt & 1)) return;
+      tc_fence_after();
+      float x[128];
+      {
+        uint32_t r[4][32];
+        tmem_ld32(tS, r[0]);
+        tmem_ld32(tS + 32, r[1]);
+        tmem_ld32(tS + 64, r[2]);
+        tmem_ld32(tS + 96, r[3]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 128; ++k) x[k] = __uint_as_float(r[k >> 5][k & 31]) * p.scale_log2;
+      }
+      const int nv = limit - kTile * j;
+      const int flags = p.page_table ? ms.flags[(tiles + j) % kFlagRing] : 0;
+      if (__any_sync(0xffffffffu, nv < kTile) || flags) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          x[k] = k < nv && !(flags >> (k >> 6) & 1) ? x[k] : -INFINITY;
+      }
+      float mx0 = fmaxf(x[0], x[1]), mx1 = fmaxf(x[2], x[3]);
+#pragma unroll
+      for (int k = 4; k < 128; k += 4) {
+        mx0 = fmaxf(mx0, fmaxf(x[k], x[k + 1]));
+        mx1 = fmaxf(mx1, fmaxf(x[k + 2], x[k + 3]));
+      }
+      const float mx = fmaxf(mx0, mx1);
+      float factor = 1.f;
+      bool resc = false;
+      if (m == -INFINITY) {
+        m = mx;
+      } else if (mx > m + kRescaleThreshold) {
+        factor = ex2(m - mx);
+        m = mx;
+        resc = true;
+      }
+      if (__any_sync(0xffffffffu, resc)) {  // O as the previous P V left it
+        l *= factor;
+        lx *= factor;
+        if (!wait(ms.pv_done[t], (cnt - 1) & 1)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < DV; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * factor);
+          tmem_st32(tO + c, o);
+        }
+        tmem_wait_st();
+      }
+      const float mu = m == -INFINITY ? 0.f : m;
+      const uint64_t one = f2_pack(1.f, 1.f), nm = f2_pack(-mu, -mu);
+      uint64_t s16 = f2_pack(0.f, 0.f), s32 = f2_pack(0.f, 0.f);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          float e0, e1;
+          f2_unpack(f2_fma(f2_pack(x[64 * h + 2 * k], x[64 * h + 2 * k + 1]), one, nm), e0, e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          pk[k] = T::pack(e0, e1);
+          const float2 e = T::unpack(pk[k]);
+          s32 = f2_add(s32, f2_pack(e0, e1));
+          s16 = f2_add(s16, f2_pack(e.x, e.y));
+        }
+        tmem_st32(tS + 32 * h, pk);  // over this row's own scores: they are in registers
+      }
+      float a, b;
+      f2_unpack(s16, a, b);
+      l += a + b;
+      f2_unpack(s32, a, b);
+      lx += a + b;
+      const int left = it.e.kvlen - kTile * j;
+      if (left < kTile) {
+        // behind the request's last key stand other rows or stale ones; a
+        // weight of 0 does not stop an infinity or a NaN there, so they are
+        // cleared before P V reads them
+        const uint32_t sv = (tiles + j) * C::kSPT + C::kNK;
+#pragma unroll
+        for (int c = 0; c < C::kNV; ++c) {
+          const uint32_t slot = (sv + c) % C::kRing;
+          if (!wait(ms.full[slot], ((sv + c) / C::kRing) & 1)) return;
+          if (row >= left)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              st_shared_v4(ring + slot * kStage + row * 128 + 16 * i, 0, 0, 0, 0);
+        }
+        fence_async_smem();
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) arrive(smem_addr(&ms.p_full[t]));
+    }
+    tiles += it.nmax;
+    if (n > 0) {
+      if (!wait(ms.pv_done[t], (cnt - 1) & 1)) return;
+      tc_fence_after();
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : NAN);
+    const int64_t orow = (int64_t)(it.e.q0 + tok) * p.o_st + (int64_t)(it.hk * p.g + head) * p.o_sh;
+#pragma unroll
+    for (int c = 0; c < DV; c += 32) {
+      uint32_t o[32];
+      if (n > 0) {
+        tmem_ld32(tO + c, o);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = 0u;
+      }
+      if (live) {
+        if (p.out_dtype == TPLA_F32) {
+          float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + orow + c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            d[k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
+                               __uint_as_float(o[4 * k + 2]) * inv,
+                               __uint_as_float(o[4 * k + 3]) * inv);
+        } else {
+          uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + orow + c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[i] = T::pack(__uint_as_float(o[8 * k + 2 * i]) * inv,
+                             __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
+            d[k] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+    }
+    if (live && p.lse)
+      p.lse[(int64_t)(it.e.q0 + tok) * p.l_st + (int64_t)(it.hk * p.g + head) * p.l_sh] =
+          lx > 0.f ? (m + log2f(lx)) * kLn2 : (lx == 0.f ? -INFINITY : NAN);
+    tc_fence_before();
+  }
+}
+
+template <typename T, int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+kv_prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
+                  const __grid_constant__ CUtensorMap vm, const Params p) {
+  using C = Cfg<T, DK, DV>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  Misc& ms = *reinterpret_cast<Misc*>(smem + C::kQ + C::kRing * kStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kRing; ++s) {
+      mbar_init(smem_addr(&ms.full[s]), 1);
+      mbar_init(smem_addr(&ms.empty[s]), 1);
+    }
+    mbar_init(smem_addr(&ms.q_full), 1);
+    mbar_init(smem_addr(&ms.q_empty), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_addr(&ms.s_full[t]), 1);
+      mbar_init(smem_addr(&ms.p_full[t]), 4);
+      mbar_init(smem_addr(&ms.pv_done[t]), 1);
+    }
+    ms.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpProd && lane == 0) {
+    tma_prefetch(&qm);
+    tma_prefetch(&km);
+    tma_prefetch(&vm);
+  }
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_addr(&ms.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&ms.tmem);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list of items
+
+  if (warp == kWarpMma) {
+    if (lane == 0) mma_issuer<T, DK, DV>(p, sbase, tmem, ms);
+  } else if (warp == kWarpProd) {
+    producer<T, DK, DV>(p, &qm, &km, &vm, sbase, ms);
+  } else if (warp >= kWarpSm0) {
+    softmax<T, DK, DV>(p, (warp - kWarpSm0) >> 2, sbase, tmem, ms);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// The list of items, longest first: a counting sort by the key tiles of each
+// item's last token.  One block; a warp takes a request at a time.  The order
+// within a bucket is not fixed, and no result depends on it.
+__global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, Entry* list,
+                                                               int* count, int capacity) {
+  __shared__ int hist[kBuckets];
+  __shared__ int top, warp_sum[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tb = 2 * p.tpt;
+  for (int i = threadIdx.x; i < kBuckets; i += 1024) hist[i] = 0;
+  if (threadIdx.x == 0) top = 0;
+  __syncthreads();
+  int most = 0;
+  for (int b = threadIdx.x; b < p.B; b += 1024) {
+    Entry e;
+    request(p, b, e);
+    most = max(most, (e.kvlen + kTile - 1) / kTile);
+  }
+  if (most) atomicMax(&top, most);
+  __syncthreads();
+  int shift = 0;
+  while ((top >> shift) >= kBuckets) ++shift;
+  auto bucket = [&](const Entry& e, int t0) {  // 0 for the longest
+    const int tiles = (limit_of(p, e, min(t0 + tb, e.qlen) - 1) + kTile - 1) / kTile;
+    return kBuckets - 1 - (tiles >> shift);
+  };
+  for (int b = warp; b < p.B; b += 32) {
+    Entry e;
+    request(p, b, e);
+    for (int t0 = lane * tb; t0 < e.qlen; t0 += 32 * tb) atomicAdd(&hist[bucket(e, t0)], 1);
+  }
+  __syncthreads();
+  {  // exclusive prefix of the buckets, two to a thread
+    const int a = hist[2 * threadIdx.x], z = hist[2 * threadIdx.x + 1];
+    int incl = a + z;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = incl - a - z;
+    for (int i = 0; i < warp; ++i) before += warp_sum[i];
+    hist[2 * threadIdx.x] = before;
+    hist[2 * threadIdx.x + 1] = before + a;
+    if (threadIdx.x == 1023) *count = min(before + a + z, capacity);
+  }
+  __syncthreads();
+  for (int b = warp; b < p.B; b += 32) {
+    Entry e;
+    request(p, b, e);
+    e.pad0 = e.pad1 = 0;
+    for (int t0 = lane * tb; t0 < e.qlen; t0 += 32 * tb) {
+      const int at = atomicAdd(&hist[bucket(e, t0)], 1);
+      if (at < capacity) {  // requests that overlap in q can ask for more
+        e.t0 = t0;
+        const int4* s = reinterpret_cast<const int4*>(&e);
+        int4* d = reinterpret_cast<int4*>(list + at);
+        d[0] = s[0];
+        d[1] = s[1];
+      } else {
+        bounds();
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+struct Shape {
+  int g, gg, groups, tpt;
+  int64_t entries;  // most items of a head: ceil(T_b / (2 tpt)) summed over the requests
+};
+
+Shape shape(const KvPrefillProblem& p) {
+  Shape s;
+  s.g = p.Hq / p.kv.Hkv;
+  s.gg = s.g < kTile ? s.g : kTile;
+  s.groups = (s.g + s.gg - 1) / s.gg;
+  s.tpt = kTile / s.gg;
+  s.entries = (int64_t)p.T / (2 * s.tpt) + p.B;
+  return s;
+}
+
+template <typename T, int DK, int DV>
+cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
+                   const Params& p, int grid, int dev, cudaStream_t stream) {
+  using C = Cfg<T, DK, DV>;
+  static std::mutex mu;
+  static uint64_t ready = 0;  // devices whose shared-memory limit is raised
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!(ready >> dev & 1)) {
+      cudaError_t e = cudaFuncSetAttribute(kv_prefill_kernel<T, DK, DV>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      if (e != cudaSuccess) return e;
+      ready |= 1ull << dev;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.count ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_prefill_kernel<T, DK, DV>, qm, km, vm, p);
+  count_launch();
+  return e;
+}
+
+template <typename T>
+cudaError_t launch_type(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
+                        const Params& p, int dk, int dv, int grid, int dev, cudaStream_t stream) {
+  if (dk == 64 && dv == 64) return launch<T, 64, 64>(qm, km, vm, p, grid, dev, stream);
+  if (dk == 128 && dv == 128) return launch<T, 128, 128>(qm, km, vm, p, grid, dev, stream);
+  if (dk == 192 && dv == 128) return launch<T, 192, 128>(qm, km, vm, p, grid, dev, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t kv_prefill_workspace_bytes(const KvPrefillProblem& p) {
+  if (p.B <= 1) return 0;
+  return 256 + (size_t)shape(p).entries * sizeof(Entry);
+}
+
+cudaError_t launch_kv_prefill(const KvPrefillProblem& dp, void* ws, cudaStream_t stream) {
+  const int dev = current_device();
+  if (!sm100_device(dev)) return cudaErrorNotSupported;
+  int sms = 0;
+  cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const KvSource& kv = dp.kv;
+  const Shape s = shape(dp);
+  CUtensorMap qm, km, vm;
+  {
+    const cuuint64_t dims[5] = {64, (cuuint64_t)s.g, (cuuint64_t)dp.T, (cuuint64_t)(kv.Dk / 64),
+                                (cuuint64_t)kv.Hkv};
+    const cuuint64_t strides[4] = {map_stride(s.g, dp.q_sh), map_stride(dp.T, dp.q_st), 128,
+                                   map_stride(kv.Hkv, dp.q_sh * s.g)};
+    const cuuint32_t box[5] = {64, (cuuint32_t)s.gg, (cuuint32_t)s.tpt, 1, 1};
+    if (!encode_16bit_5d(&qm, dp.q, kv.f16, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  const int64_t rows = kv.page_table ? kBlock : kv.cap_rows;
+  if (!encode_kv_tiles(&km, kv.k, dp.q, kv.f16, rows, kv.Hkv, kv.num_blocks, kv.k_s0, kv.k_s1,
+                       kv.k_s2, kv.Dk, 1) ||
+      !encode_kv_tiles(&vm, kv.v, dp.q, kv.f16, rows, kv.Hkv, kv.num_blocks, kv.v_s0, kv.v_s1,
+                       kv.v_s2, kv.Dv, 1))
+    return cudaErrorInvalidValue;
+  Params p{};
+  p.cu_q = dp.cu_q;
+  p.cu_k = dp.cu_k;
+  p.seq_lens = kv.seq_lens;
+  p.page_table = kv.page_table;
+  p.pt_sb = kv.pt_sb;
+  p.num_blocks = (int)kv.num_blocks;
+  p.cap_rows = (int)kv.cap_rows;
+  p.B = dp.B;
+  p.T = dp.T;
+  p.Hkv = kv.Hkv;
+  p.g = s.g;
+  p.gg = s.gg;
+  p.groups = s.groups;
+  p.tpt = s.tpt;
+  p.causal = dp.causal;
+  p.scale_log2 = (float)((double)dp.scale * 1.4426950408889634);
+  p.out = dp.out;
+  p.out_dtype = dp.out_dtype;
+  p.o_st = dp.o_st;
+  p.o_sh = dp.o_sh;
+  p.lse = dp.lse;
+  p.l_st = dp.l_st;
+  p.l_sh = dp.l_sh;
+  const int64_t items = s.entries * kv.Hkv * s.groups;
+  if (items > (1LL << 31) - 1 - sms) return cudaErrorInvalidValue;
+  if (dp.B > 1) {
+    int* count = reinterpret_cast<int*>(ws);
+    Entry* list = reinterpret_cast<Entry*>(reinterpret_cast<char*>(ws) + 256);
+    kv_prefill_plan_kernel<<<1, 1024, 0, stream>>>(p, list, count, (int)s.entries);
+    count_launch();
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    p.count = count;
+    p.list = list;
+  }
+  const int grid = (int)(items < sms ? items : sms);
+  return kv.f16 ? launch_type<F16>(qm, km, vm, p, kv.Dk, kv.Dv, grid, dev, stream)
+                : launch_type<Bf16>(qm, km, vm, p, kv.Dk, kv.Dv, grid, dev, stream);
+}
+
+cudaError_t status_read_clear_kv_prefill(int* code) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv_prefill_status, sizeof(int));
+  if (e != cudaSuccess) return e;
+  if (v != 0) {
+    int zero = 0;
+    e = cudaMemcpyToSymbol(g_kv_prefill_status, &zero, sizeof(int));
+  }
+  *code = v;
+  return e;
+}
+
+}  // namespace tpla
