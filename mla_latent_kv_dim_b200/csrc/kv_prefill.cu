@@ -40,8 +40,13 @@ __device__ int g_kv_prefill_status;
 constexpr int kTile = 128;     // rows of a query tile, keys of a key tile
 constexpr int kStage = 16384;  // 128 keys x 64 columns
 constexpr int kThreads = 384;
-constexpr int kWarpMma = 0, kWarpProd = 1, kWarpSm0 = 4;  // 4-7: tile A, 8-11: tile B
+constexpr int kWarpMma = 0, kWarpProd = 1, kWarpQ = 2, kWarpSm0 = 4;  // 4-7: tile A, 8-11: tile B
+// Registers move to the softmax warpgroups, whose threads hold a row of 128
+// scores: 384 x 168 at launch = 128 x 88 + 256 x 208.
+constexpr int kRegsOther = 88, kRegsSoftmax = 208;
+static_assert(128 * kRegsOther + 256 * kRegsSoftmax <= kThreads * 168, "register split");
 constexpr int kMaxRing = 12;
+constexpr int kParts = 16;     // barriers of parts in flight (at most kMaxRing parts are)
 constexpr int kFlagRing = 8;   // key tiles whose page flags are kept (ring / stages of a tile < 8)
 constexpr int kSmemBytes = 232448;
 constexpr int kMiscBytes = 2048;
@@ -64,7 +69,8 @@ struct Params {
   int cap_rows;
   int B, T, Hkv, g, gg, groups, tpt;  // gg heads of a row group, tpt tokens of a tile
   int causal;
-  float scale_log2;
+  float scale_log2;      // |softmax scale| * log2(e) (> 0; see the launcher)
+  int negate;            // scale < 0
   const int* count;      // entries of the list, or null: one request, no list
   const Entry* list;
   void* out;
@@ -126,27 +132,48 @@ __device__ __forceinline__ int item_count(const Params& p) {
   return n * p.Hkv * p.groups;
 }
 
-__device__ __forceinline__ void get_item(const Params& p, int idx, int total, Item& it) {
-  const int heads = p.Hkv * p.groups;
-  const int x = idx / heads, h = idx - x * heads;
-  it.hk = h / p.groups;
-  it.rg = h - it.hk * p.groups;
-  if (p.count) {
-    const int4* s = reinterpret_cast<const int4*>(p.list + x);
-    int4* d = reinterpret_cast<int4*>(&it.e);
-    d[0] = s[0];
-    d[1] = s[1];
-  } else {  // longest first: the last tokens of a causal prompt see the most keys
-    request(p, 0, it.e);
-    it.e.t0 = (total / heads - 1 - x) * 2 * p.tpt;
+// A block's items: every gridDim.x-th of the list, in alternating direction
+// so that the blocks with the longest of one round get the shortest of the
+// next.
+struct Items {
+  int total, heads, round;
+  __device__ explicit Items(const Params& p)
+      : total(item_count(p)), heads(p.Hkv * p.groups), round(0) {}
+
+  // the next item with keys, or (want_empty) the next of any kind
+  __device__ bool next(const Params& p, Item& it, bool want_empty = false) {
+    for (;;) {
+      const int c = round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+      const long long idx = (long long)round * gridDim.x + c;
+      if ((long long)round * gridDim.x >= total) return false;
+      ++round;
+      if (idx >= total) continue;
+      get(p, (int)idx, it);
+      if (it.nmax > 0 || want_empty) return true;
+    }
   }
+
+  __device__ void get(const Params& p, int idx, Item& it) const {
+    const int x = idx / heads, h = idx - x * heads;
+    it.hk = h / p.groups;
+    it.rg = h - it.hk * p.groups;
+    if (p.count) {
+      const int4* s = reinterpret_cast<const int4*>(p.list + x);
+      int4* d = reinterpret_cast<int4*>(&it.e);
+      d[0] = s[0];
+      d[1] = s[1];
+    } else {  // longest first: the last tokens of a causal prompt see the most keys
+      request(p, 0, it.e);
+      it.e.t0 = (total / heads - 1 - x) * 2 * p.tpt;
+    }
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int a = it.e.t0 + t * p.tpt, z = min(a + p.tpt, it.e.qlen);
-    it.n[t] = z > a ? (limit_of(p, it.e, z - 1) + kTile - 1) / kTile : 0;
+    for (int t = 0; t < 2; ++t) {
+      const int a = it.e.t0 + t * p.tpt, z = min(a + p.tpt, it.e.qlen);
+      it.n[t] = z > a ? (limit_of(p, it.e, z - 1) + kTile - 1) / kTile : 0;
+    }
+    it.nmax = max(it.n[0], it.n[1]);
   }
-  it.nmax = max(it.n[0], it.n[1]);
-}
+};
 
 template <typename T, int DK, int DV>
 struct Cfg {
@@ -165,44 +192,58 @@ struct Cfg {
 };
 
 struct Misc {
-  unsigned long long full[kMaxRing], empty[kMaxRing];
-  unsigned long long q_full, q_empty, s_full[2], p_full[2], pv_done[2];
+  // K and V of a key tile are parts 2 j and 2 j + 1 (of all key tiles of the
+  // block): one barrier says that a part has landed, one per stage that the
+  // stage may be written again
+  unsigned long long full[kParts], empty[kMaxRing];
+  unsigned long long q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
   int flags[kFlagRing];
   uint32_t tmem;
   int abort_flag;
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc shared memory");
 
+// Query tiles: each as soon as the last Q K^T of the tile before it is done.
 template <typename T, int DK, int DV>
-__device__ void producer(const Params& p, const CUtensorMap* qm, const CUtensorMap* km,
-                         const CUtensorMap* vm, uint32_t sbase, Misc& ms) {
+__device__ void q_producer(const Params& p, const CUtensorMap* qm, uint32_t sbase, Misc& ms) {
+  using C = Cfg<T, DK, DV>;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &ms.abort_flag;
+  Items items(p);
+  Item it;
+  uint32_t loads[2] = {0, 0};
+  while (items.next(p, it)) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (it.n[t] == 0) continue;
+      const uint32_t qf = smem_addr(&ms.q_full[t]);
+      int ok = 1;
+      if (lane == 0) {
+        if (loads[t] > 0)
+          ok = wait_bar(smem_addr(&ms.q_empty[t]), (loads[t] - 1) & 1, abort_flag,
+                        &g_kv_prefill_status);
+        if (ok) mbar_arrive_expect_tx(qf, C::kNK * p.gg * p.tpt * 128);
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+      ++loads[t];
+      if (lane < C::kNK)
+        tma_load_5d(sbase + (t * C::kNK + lane) * kStage, qm, 0, it.rg * p.gg,
+                    it.e.q0 + it.e.t0 + t * p.tpt, lane, it.hk, qf);
+    }
+  }
+}
+
+template <typename T, int DK, int DV>
+__device__ void producer(const Params& p, const CUtensorMap* km, const CUtensorMap* vm,
+                         uint32_t sbase, Misc& ms) {
   using C = Cfg<T, DK, DV>;
   const int lane = threadIdx.x & 31;
   const uint32_t ring = sbase + C::kQ;
   volatile int* abort_flag = &ms.abort_flag;
-  const int total = item_count(p);
-  uint32_t n = 0, qloads = 0, tile = 0;
-  for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
-    Item it;
-    get_item(p, idx, total, it);
-    if (it.nmax == 0) continue;
-    int ok = 1;
-    if (lane == 0 && qloads > 0)
-      ok = wait_bar(smem_addr(&ms.q_empty), (qloads - 1) & 1, abort_flag, &g_kv_prefill_status);
-    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
-    ++qloads;
-    const uint32_t qf = smem_addr(&ms.q_full);
-    if (lane == 0) {
-      const int tiles = (it.n[0] > 0) + (it.n[1] > 0);
-      mbar_arrive_expect_tx(qf, tiles * C::kNK * p.gg * p.tpt * 128);
-    }
-    __syncwarp();
-    if (lane < 2 * C::kNK) {
-      const int t = lane / C::kNK, c = lane - t * C::kNK;
-      if (it.n[t] > 0)
-        tma_load_5d(sbase + lane * kStage, qm, 0, it.rg * p.gg, it.e.q0 + it.e.t0 + t * p.tpt, c,
-                    it.hk, qf);
-    }
+  Items items(p);
+  Item it;
+  uint32_t n = 0, tile = 0;
+  while (items.next(p, it)) {
     int win = 0;  // lane i: page id 32 w + i
     for (int j = 0; j < it.nmax; ++j, ++tile) {
       int pg[2] = {0, 0}, row[2] = {it.e.k0 + kTile * j, it.e.k0 + kTile * j + 64};
@@ -217,7 +258,7 @@ __device__ void producer(const Params& p, const CUtensorMap* qm, const CUtensorM
         for (int h = 0; h < 2; ++h) {
           const int id = __shfl_sync(0xffffffffu, win, (2 * j + h) & 31);
           const bool good = id >= 0 && id < p.num_blocks;
-          if (id != -2 || 2 * j + h < pages) flags |= good ? 0 : 1 << h;
+          if (2 * j + h < pages) flags |= good ? 0 : 1 << h;
           pg[h] = good ? id : max(p.num_blocks, 1);  // past the last page: reads as zeros
           row[h] = 0;
         }
@@ -226,26 +267,37 @@ __device__ void producer(const Params& p, const CUtensorMap* qm, const CUtensorM
           ms.flags[tile % kFlagRing] = flags;
         }
       }
-      for (int st = 0; st < C::kSPT; ++st, ++n) {
-        const uint32_t slot = n % C::kRing;
-        ok = 1;
-        if (lane == 0 && n >= C::kRing)
-          ok = wait_bar(smem_addr(&ms.empty[slot]), ((n / C::kRing) - 1) & 1, abort_flag,
-                        &g_kv_prefill_status);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) return;
-        const uint32_t full = smem_addr(&ms.full[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(full, kStage);
-        __syncwarp();
-        if (lane < 2) {
-          const int c = st < C::kNK ? st : st - C::kNK;
-          tma_load_5d(ring + slot * kStage + lane * (kStage / 2), st < C::kNK ? km : vm, 0,
-                      lane ? row[1] : row[0], c, it.hk, lane ? pg[1] : pg[0], full);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        constexpr int kN[2] = {C::kNK, C::kNV};
+        const uint32_t full = smem_addr(&ms.full[(2 * tile + v) % kParts]);
+        for (int c = 0; c < kN[v]; ++c, ++n) {
+          const uint32_t slot = n % C::kRing;
+          int ok = 1;
+          if (lane == 0 && n >= C::kRing)
+            ok = wait_bar(smem_addr(&ms.empty[slot]), ((n / C::kRing) - 1) & 1, abort_flag,
+                          &g_kv_prefill_status);
+          if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+          if (lane == 0 && c == 0) mbar_arrive_expect_tx(full, kN[v] * kStage);
+          __syncwarp();
+          if (lane < 2)
+            tma_load_5d(ring + slot * kStage + lane * (kStage / 2), v ? vm : km, 0,
+                        lane ? row[1] : row[0], c, it.hk, lane ? pg[1] : pg[0], full);
         }
       }
     }
   }
 }
 
+// Both products of both tiles, in one order: for each key tile j, tile A then
+// tile B: O += P V_j, then at once the tile's next S = Q K^T (key tile j + 1,
+// or key tile 0 of the next item), so that the tensor core has the other
+// tile's products to do while a softmax runs, across items too.
+//
+// What the tensor core waits for is this thread: every wait and every commit
+// costs it some 150 cycles, so there are few.  One commit per step (s_full)
+// says all: the products complete in order, so S of key tile j + 1 also means
+// that P V_j is done, and the softmax threads that see it free K and V.
 template <typename T, int DK, int DV>
 __device__ void mma_issuer(const Params& p, uint32_t sbase, uint32_t tmem, Misc& ms) {
   using C = Cfg<T, DK, DV>;
@@ -258,83 +310,80 @@ __device__ void mma_issuer(const Params& p, uint32_t sbase, uint32_t tmem, Misc&
   const uint32_t q_lo = (uint32_t)dQ, k_lo = (uint32_t)dK, kk_hi = (uint32_t)(dK >> 32);
   const uint32_t v_lo = (uint32_t)dV, v_hi = (uint32_t)(dV >> 32);
   constexpr uint32_t kS = kStage >> 4;
-  const int total = item_count(p);
-  uint32_t base = 0, qloads = 0, cnt[2] = {0, 0};
+  uint32_t tile = 0, slot = 0;  // key tiles before this one; ring slot of its K
+  uint32_t qloads[2] = {0, 0}, cnt[2] = {0, 0};
   auto wait = [&](unsigned long long& bar, uint32_t parity) {
     return wait_bar(smem_addr(&bar), parity, abort_flag, &g_kv_prefill_status);
   };
-  auto wait_stages = [&](uint32_t s, int k) {
-    for (int i = 0; i < k; ++i)
-      if (!wait(ms.full[(s + i) % C::kRing], ((s + i) / C::kRing) & 1)) return false;
+  auto wait_part = [&](uint32_t part) {
+    return wait(ms.full[part % kParts], (part / kParts) & 1);
+  };
+  auto wrap = [](uint32_t s) { return s >= C::kRing ? s - C::kRing : s; };
+  // S of tile t and key tile j of item `it`, whose K begins at ring slot s
+  auto qk = [&](const Item& it, int t, int j, uint32_t part, uint32_t s) {
+    if (j == 0) {
+      if (!wait(ms.q_full[t], qloads[t] & 1)) return false;
+      ++qloads[t];
+    }
+    if ((t == 0 || j >= it.n[0]) && !wait_part(part)) return false;  // tile A has waited for B
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < C::kNK; ++c) {
+      const uint32_t a = q_lo + (uint32_t)(t * C::kNK + c) * kS;
+      const uint32_t b = k_lo + wrap(s + c) * kS;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mma_ss(tmem + kColS + kTile * t, a + 2 * k, kk_hi, b + 2 * k, kk_hi, C::idesc(128, false),
+               (c | k) != 0);
+    }
+    commit(smem_addr(&ms.s_full[t]));
+    if (j + 1 == it.n[t]) commit(smem_addr(&ms.q_empty[t]));
     return true;
   };
-  auto release = [&](uint32_t s, int k) {
-    for (int i = 0; i < k; ++i) commit(smem_addr(&ms.empty[(s + i) % C::kRing]));
-  };
-  for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
-    Item it;
-    get_item(p, idx, total, it);
-    if (it.nmax == 0) continue;
-    auto qk = [&](int t, uint32_t s) {
+  Items items(p);
+  Item it, nx;
+  if (!items.next(p, it)) return;
 #pragma unroll
-      for (int c = 0; c < C::kNK; ++c) {
-        const uint32_t a = q_lo + (uint32_t)(t * C::kNK + c) * kS;
-        const uint32_t b = k_lo + ((s + c) % C::kRing) * kS;
+  for (int t = 0; t < 2; ++t)
+    if (it.n[t] > 0 && !qk(it, t, 0, 0, 0)) return;
+  for (bool more = true; more;) {
+    more = items.next(p, nx);
+    for (int j = 0; j < it.nmax; ++j, ++tile) {
+      const uint32_t sv = wrap(slot + C::kNK), sn = wrap(sv + C::kNV);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss(tmem + kColS + kTile * t, a + 2 * k, kk_hi, b + 2 * k, kk_hi,
-                 C::idesc(128, false), (c | k) != 0);
-      }
-      commit(smem_addr(&ms.s_full[t]));
-    };
-    if (!wait(ms.q_full, qloads & 1)) return;
-    ++qloads;
-    if (!wait_stages(base, C::kNK)) return;
-    tc_fence_after();
-    for (int t = 0; t < 2; ++t)
-      if (it.n[t] > 0) qk(t, base);
-    release(base, C::kNK);
-    if (it.nmax == 1) commit(smem_addr(&ms.q_empty));
-    for (int j = 0; j < it.nmax; ++j) {
-      const uint32_t s = base + (uint32_t)j * C::kSPT, sv = s + C::kNK, sn = s + C::kSPT;
       for (int t = 0; t < 2; ++t) {
-        if (j >= it.n[t]) continue;
-        const bool first = t == 0 || j >= it.n[0], last = t == 1 || j >= it.n[1];
-        if (!wait(ms.p_full[t], cnt[t] & 1)) return;
-        ++cnt[t];
-        if (first && !wait_stages(sv, C::kNV)) return;
-        tc_fence_after();
-        const uint32_t pa = tmem + kColS + kTile * t;
-        const uint32_t dO = tmem + kColO + kTile * t;
-        const uint32_t slot = sv % C::kRing;
-        if (C::kNV == 1 || slot + 1 < C::kRing) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts(dO, pa + 8 * k, v_lo + slot * kS + 128 * k, v_hi, C::idesc(DV, true),
-                   (j | k) != 0);
-        } else {  // the chunks lie at the ring's end and its beginning
-#pragma unroll
-          for (int c = 0; c < C::kNV; ++c)
+        if (j < it.n[t]) {
+          if ((t == 0 || j >= it.n[0]) && !wait_part(2 * tile + 1)) return;
+          if (!wait(ms.p_full[t], cnt[t] & 1)) return;
+          ++cnt[t];
+          tc_fence_after();
+          const uint32_t pa = tmem + kColS + kTile * t;
+          const uint32_t dO = tmem + kColO + kTile * t;
+          if (C::kNV == 1 || sv + 1 < C::kRing) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              mma_ts(dO + 64 * c, pa + 8 * k, v_lo + ((sv + c) % C::kRing) * kS + 128 * k, v_hi,
-                     C::idesc(64, true), (j | k) != 0);
-        }
-        commit(smem_addr(&ms.pv_done[t]));
-        if (last) release(sv, C::kNV);
-        if (j + 1 < it.n[t]) {
-          const bool nfirst = t == 0 || j + 1 >= it.n[0], nlast = t == 1 || j + 1 >= it.n[1];
-          if (nfirst && !wait_stages(sn, C::kNK)) return;
-          tc_fence_after();
-          qk(t, sn);
-          if (nlast) {
-            release(sn, C::kNK);
-            if (j + 2 == it.nmax) commit(smem_addr(&ms.q_empty));
+              mma_ts(dO, pa + 8 * k, v_lo + sv * kS + 128 * k, v_hi, C::idesc(DV, true),
+                     (j | k) != 0);
+          } else {  // the chunks lie at the ring's end and its beginning
+#pragma unroll
+            for (int c = 0; c < C::kNV; ++c)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_ts(dO + 64 * c, pa + 8 * k, v_lo + wrap(sv + c) * kS + 128 * k, v_hi,
+                       C::idesc(64, true), (j | k) != 0);
+          }
+          if (j + 1 < it.n[t]) {
+            if (!qk(it, t, j + 1, 2 * tile + 2, sn)) return;
+          } else {
+            commit(smem_addr(&ms.o_full[t]));
           }
         }
+        // the ring holds this item's last V and the next item's first K
+        if (j + 1 == it.nmax && more && nx.n[t] > 0 && !qk(nx, t, 0, 2 * tile + 2, sn)) return;
       }
+      slot = sn;
     }
-    base += (uint32_t)it.nmax * C::kSPT;
+    it = nx;
   }
 }
 
@@ -348,26 +397,36 @@ __device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, M
   const uint32_t tS = tmem + lane_base + kColS + kTile * t;
   const uint32_t tO = tmem + lane_base + kColO + kTile * t;
   const uint32_t ring = sbase + C::kQ;
-  const int total = item_count(p);
   const int my_tok = row / p.gg, my_head = row - my_tok * p.gg;
-  uint32_t cnt = 0, tiles = 0;
+  uint32_t cnt = 0, tiles = 0, done = 0;
+  // frees the stages of a part whose last reader is this tile
+  auto release = [&](uint32_t tile, int v) {
+    if ((threadIdx.x & 127) == 0) {
+      const uint32_t s = tile * C::kSPT + (v ? C::kNK : 0);
+      for (int c = 0; c < (v ? C::kNV : C::kNK); ++c)
+        arrive(smem_addr(&ms.empty[(s + c) % C::kRing]));
+    }
+  };
   auto wait = [&](unsigned long long& bar, uint32_t parity) {
     const bool ok = wait_bar(smem_addr(&bar), parity, abort_flag, &g_kv_prefill_status);
     return __all_sync(0xffffffffu, ok) != 0;
   };
-  for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
-    Item it;
-    get_item(p, idx, total, it);
+  Items items(p);
+  Item it;
+  while (items.next(p, it, true)) {
     const int tok = it.e.t0 + t * p.tpt + my_tok;
     const int head = it.rg * p.gg + my_head;
     const bool live = my_tok < p.tpt && tok < it.e.qlen && head < p.g;
     // rows past the tile's tokens or the request's are computed and not stored
     const int limit = live ? limit_of(p, it.e, tok) : it.e.kvlen;
-    const int n = it.n[t];
+    const int n = t ? it.n[1] : it.n[0];
     float m = -INFINITY, l = 0.f, lx = 0.f;  // maximum; sums of the 16-bit and the f32 weights
     for (int j = 0; j < n; ++j, ++cnt) {
       if (!wait(ms.s_full[t], cnt & 1)) return;
       tc_fence_after();
+      // this S is done, and with it the P V before it
+      if (t == 1 || j >= it.n[1]) release(tiles + j, 0);
+      if (j > 0 && (t == 1 || j - 1 >= it.n[1])) release(tiles + j - 1, 1);
       float x[128];
       {
         uint32_t r[4][32];
@@ -377,7 +436,11 @@ __device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, M
         tmem_ld32(tS + 96, r[3]);
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 128; ++k) x[k] = __uint_as_float(r[k >> 5][k & 31]) * p.scale_log2;
+        for (int k = 0; k < 128; ++k) x[k] = __uint_as_float(r[k >> 5][k & 31]);
+      }
+      if (p.negate) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k) x[k] = -x[k];
       }
       const int nv = limit - kTile * j;
       const int flags = p.page_table ? ms.flags[(tiles + j) % kFlagRing] : 0;
@@ -386,13 +449,14 @@ __device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, M
         for (int k = 0; k < 128; ++k)
           x[k] = k < nv && !(flags >> (k >> 6) & 1) ? x[k] : -INFINITY;
       }
-      float mx0 = fmaxf(x[0], x[1]), mx1 = fmaxf(x[2], x[3]);
+      float mxs[4];
 #pragma unroll
-      for (int k = 4; k < 128; k += 4) {
-        mx0 = fmaxf(mx0, fmaxf(x[k], x[k + 1]));
-        mx1 = fmaxf(mx1, fmaxf(x[k + 2], x[k + 3]));
+      for (int i = 0; i < 4; ++i) {
+        mxs[i] = fmaxf(x[2 * i], x[2 * i + 1]);
+#pragma unroll
+        for (int k = 8 + 2 * i; k < 128; k += 8) mxs[i] = max3(mxs[i], x[k], x[k + 1]);
       }
-      const float mx = fmaxf(mx0, mx1);
+      const float mx = fmaxf(max3(mxs[0], mxs[1], mxs[2]), mxs[3]) * p.scale_log2;
       float factor = 1.f;
       bool resc = false;
       if (m == -INFINITY) {
@@ -405,8 +469,6 @@ __device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, M
       if (__any_sync(0xffffffffu, resc)) {  // O as the previous P V left it
         l *= factor;
         lx *= factor;
-        if (!wait(ms.pv_done[t], (cnt - 1) & 1)) return;
-        tc_fence_after();
 #pragma unroll
         for (int c = 0; c < DV; c += 32) {
           uint32_t o[32];
@@ -419,7 +481,7 @@ __device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, M
         tmem_wait_st();
       }
       const float mu = m == -INFINITY ? 0.f : m;
-      const uint64_t one = f2_pack(1.f, 1.f), nm = f2_pack(-mu, -mu);
+      const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
       uint64_t s16 = f2_pack(0.f, 0.f), s32 = f2_pack(0.f, 0.f);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -427,7 +489,7 @@ __device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, M
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
           float e0, e1;
-          f2_unpack(f2_fma(f2_pack(x[64 * h + 2 * k], x[64 * h + 2 * k + 1]), one, nm), e0, e1);
+          f2_unpack(f2_fma(f2_pack(x[64 * h + 2 * k], x[64 * h + 2 * k + 1]), sc, nm), e0, e1);
           e0 = ex2(e0);
           e1 = ex2(e1);
           pk[k] = T::pack(e0, e1);
@@ -447,11 +509,11 @@ __device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, M
         // behind the request's last key stand other rows or stale ones; a
         // weight of 0 does not stop an infinity or a NaN there, so they are
         // cleared before P V reads them
-        const uint32_t sv = (tiles + j) * C::kSPT + C::kNK;
+        const uint32_t sv = (tiles + j) * C::kSPT + C::kNK, part = 2 * (tiles + j) + 1;
+        if (!wait(ms.full[part % kParts], (part / kParts) & 1)) return;
 #pragma unroll
         for (int c = 0; c < C::kNV; ++c) {
           const uint32_t slot = (sv + c) % C::kRing;
-          if (!wait(ms.full[slot], ((sv + c) / C::kRing) & 1)) return;
           if (row >= left)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -464,11 +526,13 @@ __device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, M
       __syncwarp();
       if ((threadIdx.x & 31) == 0) arrive(smem_addr(&ms.p_full[t]));
     }
-    tiles += it.nmax;
     if (n > 0) {
-      if (!wait(ms.pv_done[t], (cnt - 1) & 1)) return;
+      if (!wait(ms.o_full[t], done & 1)) return;
+      ++done;
       tc_fence_after();
+      if (t == 1 || n > it.n[1]) release(tiles + n - 1, 1);
     }
+    tiles += it.nmax;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : NAN);
     const int64_t orow = (int64_t)(it.e.q0 + tok) * p.o_st + (int64_t)(it.hk * p.g + head) * p.o_sh;
 #pragma unroll
@@ -522,16 +586,14 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant_
   Misc& ms = *reinterpret_cast<Misc*>(smem + C::kQ + C::kRing * kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kRing; ++s) {
-      mbar_init(smem_addr(&ms.full[s]), 1);
-      mbar_init(smem_addr(&ms.empty[s]), 1);
-    }
-    mbar_init(smem_addr(&ms.q_full), 1);
-    mbar_init(smem_addr(&ms.q_empty), 1);
+    for (int s = 0; s < kParts; ++s) mbar_init(smem_addr(&ms.full[s]), 1);
+    for (int s = 0; s < C::kRing; ++s) mbar_init(smem_addr(&ms.empty[s]), 1);
     for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_addr(&ms.q_full[t]), 1);
+      mbar_init(smem_addr(&ms.q_empty[t]), 1);
       mbar_init(smem_addr(&ms.s_full[t]), 1);
       mbar_init(smem_addr(&ms.p_full[t]), 4);
-      mbar_init(smem_addr(&ms.pv_done[t]), 1);
+      mbar_init(smem_addr(&ms.o_full[t]), 1);
     }
     ms.abort_flag = 0;
     fence_mbar_init();
@@ -553,12 +615,18 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant_
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&ms.tmem);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the list of items
 
-  if (warp == kWarpMma) {
-    if (lane == 0) mma_issuer<T, DK, DV>(p, sbase, tmem, ms);
-  } else if (warp == kWarpProd) {
-    producer<T, DK, DV>(p, &qm, &km, &vm, sbase, ms);
-  } else if (warp >= kWarpSm0) {
+  if (warp >= kWarpSm0) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     softmax<T, DK, DV>(p, (warp - kWarpSm0) >> 2, sbase, tmem, ms);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == kWarpMma) {
+      if (lane == 0) mma_issuer<T, DK, DV>(p, sbase, tmem, ms);
+    } else if (warp == kWarpProd) {
+      producer<T, DK, DV>(p, &km, &vm, sbase, ms);
+    } else if (warp == kWarpQ) {
+      q_producer<T, DK, DV>(p, &qm, sbase, ms);
+    }
   }
   __syncwarp();
   tc_fence_before();
@@ -739,7 +807,11 @@ cudaError_t launch_kv_prefill(const KvPrefillProblem& dp, void* ws, cudaStream_t
   p.groups = s.groups;
   p.tpt = s.tpt;
   p.causal = dp.causal;
-  p.scale_log2 = (float)((double)dp.scale * 1.4426950408889634);
+  // The row maximum is taken of the raw scores, negated for a negative scale.
+  // A zero scale becomes 1e-30: every finite score gives exp2(~0) = 1 exactly
+  // in f32, masked (-inf) ones still 0.
+  p.scale_log2 = fmaxf((float)(fabs((double)dp.scale) * 1.4426950408889634), 1e-30f);
+  p.negate = dp.scale < 0.f;
   p.out = dp.out;
   p.out_dtype = dp.out_dtype;
   p.o_st = dp.o_st;

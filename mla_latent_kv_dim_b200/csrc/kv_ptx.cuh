@@ -20,11 +20,25 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr long long kTimeoutCycles = 4000000000LL;  // about 2 s at full clock
 constexpr uint32_t kWaitSleepNs = 100000;           // suspend hint of one barrier poll
 
+// Wait for a barrier whose arrivals all come from this CTA (its threads, its
+// copies, its tensor core).
+__device__ __forceinline__ bool mbar_try_wait_cta(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Bounded wait: after kTimeoutCycles the thread records the timeout, raises
 // the CTA's abort flag (which ends the other roles' waits) and gives up.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait_cta(bar, parity)) return true;
   const long long t0 = clock64();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
@@ -87,6 +101,12 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    bar)
                : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // Packed two-lane float arithmetic (sm_100): one instruction for two values.
