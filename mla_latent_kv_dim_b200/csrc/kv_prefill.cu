@@ -11,14 +11,19 @@
 //  * a tile is 128 rows: tpt = 128 / g tokens times the g query heads of one
 //    key head (row = token * g + head), so that grouped heads share every
 //    key and value tile and few tokens still fill the rows;
-//  * a work item is two such tiles A and B of consecutive tokens.  One thread
-//    issues S = Q K^T (N = 128 keys) and O += P V for both in turn; while the
-//    tensor core works on one, the other's softmax warpgroup turns its S into
-//    P.  S and P share TMEM columns (P goes over S as 16-bit pairs, the A
-//    operand from TMEM), O stays in TMEM: 2 x (128 + Dv) of the 512 columns;
+//  * a work item is two such tiles A and B of consecutive tokens, which share
+//    the key tiles of 64 keys.  Each has an issuing thread, a softmax
+//    warpgroup, O in TMEM and two S buffers of 64 columns there: while the
+//    softmax works on one S the tensor core fills the other, so neither waits
+//    out the other's latency.  P goes over its own S as 16-bit pairs, the A
+//    operand from TMEM: 2 x (128 + Dv) of the 512 columns in all.  (With one S
+//    of 128 keys, Q K^T had to wait for P V, P V for the softmax and the
+//    softmax for Q K^T: 4450 cycles for 128 keys of both tiles against 2048 of
+//    tensor work.  N = 64 costs 48 cycles where N = 128 costs 64, because Q
+//    is read again.)
 //  * a thread owns a row: no exchange for the row maximum.  O is rescaled
 //    only when the maximum has grown by more than 2^8;
-//  * K and V tiles go through one ring of 16 KB stages (128 keys x 64 columns,
+//  * K and V tiles go through a ring of key tiles (64-column chunks of 64 rows,
 //    128-byte swizzle, K-major for Q K^T and MN-major for P V);
 //  * items are handed out longest first (a small kernel sorts them; one
 //    request needs no sorting), so the last ones are short.
@@ -37,17 +42,15 @@ using namespace kvx;
 
 __device__ int g_kv_prefill_status;
 
-constexpr int kTile = 128;     // rows of a query tile, keys of a key tile
-constexpr int kStage = 16384;  // 128 keys x 64 columns
+constexpr int kRows = 128;    // rows of a query tile
+constexpr int kKeys = 64;     // keys of a key tile
+constexpr int kChunk = 8192;  // 64 keys x 64 columns
 constexpr int kThreads = 384;
-constexpr int kWarpMma = 0, kWarpProd = 1, kWarpQ = 2, kWarpSm0 = 4;  // 4-7: tile A, 8-11: tile B
-// Registers move to the softmax warpgroups, whose threads hold a row of 128
-// scores: 384 x 168 at launch = 128 x 88 + 256 x 208.
-constexpr int kRegsOther = 88, kRegsSoftmax = 208;
-static_assert(128 * kRegsOther + 256 * kRegsSoftmax <= kThreads * 168, "register split");
-constexpr int kMaxRing = 12;
-constexpr int kParts = 16;     // barriers of parts in flight (at most kMaxRing parts are)
-constexpr int kFlagRing = 8;   // key tiles whose page flags are kept (ring / stages of a tile < 8)
+// Warps 0 and 1 issue the products of query tiles A and B, 4-7 and 8-11 are
+// their softmax warpgroups; 2 loads key tiles, 3 query tiles.
+constexpr int kWarpMma = 0, kWarpProd = 2, kWarpSm0 = 4;
+constexpr int kMaxRing = 12;   // key tiles
+constexpr int kFlagRing = 16;  // key tiles whose page flags are kept (> kMaxRing + 2)
 constexpr int kSmemBytes = 232448;
 constexpr int kMiscBytes = 2048;
 constexpr int kBuckets = 2048;  // of the items' lengths
@@ -169,22 +172,28 @@ struct Items {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int a = it.e.t0 + t * p.tpt, z = min(a + p.tpt, it.e.qlen);
-      it.n[t] = z > a ? (limit_of(p, it.e, z - 1) + kTile - 1) / kTile : 0;
+      it.n[t] = z > a ? (limit_of(p, it.e, z - 1) + kKeys - 1) / kKeys : 0;
     }
     it.nmax = max(it.n[0], it.n[1]);
+    // A query tile that sees no key, or has no rows, takes part with all its
+    // scores masked or unused: so the two tiles are never more than two key
+    // tiles apart (128 tokens), and no barrier is waited for from two phases
+    // away, where its parity would say the wrong thing.
+    if (it.n[0] == 0) it.n[0] = it.nmax;
+    if (it.n[1] == 0) it.n[1] = it.nmax;
   }
 };
 
 template <typename T, int DK, int DV>
 struct Cfg {
   static constexpr int kNK = DK / 64, kNV = DV / 64;  // 64-column chunks
-  static constexpr int kSPT = kNK + kNV;              // ring stages of a key tile
-  static constexpr int kQ = 2 * kNK * kStage;         // both query tiles
-  static constexpr int kRing0 = (kSmemBytes - 1024 - kMiscBytes - kQ) / kStage;
+  static constexpr int kQTile = kNK * kRows * 128;    // bytes of a query tile
+  static constexpr int kKV = (kNK + kNV) * kChunk;    // bytes of a key tile
+  static constexpr int kRing0 = (kSmemBytes - 1024 - kMiscBytes - 2 * kQTile) / kKV;
   static constexpr int kRing = kRing0 < kMaxRing ? kRing0 : kMaxRing;
-  static constexpr int kSmem = 1024 + kQ + kRing * kStage + kMiscBytes;
-  static_assert(kSmem <= kSmemBytes && kRing > kSPT, "shared memory");
-  static_assert((kRing + kSPT - 1) / kSPT + 1 < kFlagRing, "page flags");
+  static constexpr int kSmem = 1024 + 2 * kQTile + kRing * kKV + kMiscBytes;
+  // Q K^T runs two key tiles ahead of P V
+  static_assert(kSmem <= kSmemBytes && kRing >= 3, "shared memory");
   static constexpr uint32_t idesc(int n, bool b_mn) {
     return (1u << 4) | ((uint32_t)T::kFormat << 7) | ((uint32_t)T::kFormat << 10) |
            ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -192,11 +201,11 @@ struct Cfg {
 };
 
 struct Misc {
-  // K and V of a key tile are parts 2 j and 2 j + 1 (of all key tiles of the
-  // block): one barrier says that a part has landed, one per stage that the
-  // stage may be written again
-  unsigned long long full[kParts], empty[kMaxRing];
-  unsigned long long q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+  // per ring slot, K and V: landed; no longer needed by either query tile
+  unsigned long long full[kMaxRing][2], empty[kMaxRing][2];
+  unsigned long long q_full[2], q_empty[2];
+  unsigned long long o_last[2], o_full[2];  // the item's last P V but one, its last
+  unsigned long long s_full[2][2], p_full[2][2];  // per query tile and S buffer
   int flags[kFlagRing];
   uint32_t tmem;
   int abort_flag;
@@ -215,7 +224,6 @@ __device__ void q_producer(const Params& p, const CUtensorMap* qm, uint32_t sbas
   while (items.next(p, it)) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (it.n[t] == 0) continue;
       const uint32_t qf = smem_addr(&ms.q_full[t]);
       int ok = 1;
       if (lane == 0) {
@@ -227,185 +235,202 @@ __device__ void q_producer(const Params& p, const CUtensorMap* qm, uint32_t sbas
       if (!__shfl_sync(0xffffffffu, ok, 0)) return;
       ++loads[t];
       if (lane < C::kNK)
-        tma_load_5d(sbase + (t * C::kNK + lane) * kStage, qm, 0, it.rg * p.gg,
+        tma_load_5d(sbase + t * C::kQTile + lane * kRows * 128, qm, 0, it.rg * p.gg,
                     it.e.q0 + it.e.t0 + t * p.tpt, lane, it.hk, qf);
     }
   }
 }
 
+// Key tiles: a chunk from a lane of its own, because a thread's copies land
+// one after another.
 template <typename T, int DK, int DV>
 __device__ void producer(const Params& p, const CUtensorMap* km, const CUtensorMap* vm,
                          uint32_t sbase, Misc& ms) {
   using C = Cfg<T, DK, DV>;
   const int lane = threadIdx.x & 31;
-  const uint32_t ring = sbase + C::kQ;
   volatile int* abort_flag = &ms.abort_flag;
   Items items(p);
   Item it;
-  uint32_t n = 0, tile = 0;
+  uint32_t slot = 0, phase = 1;
+  uint32_t tile = 0;
   while (items.next(p, it)) {
-    int win = 0;  // lane i: page id 32 w + i
+    int win = 0;  // lane i: the page id of key tile 32 w + i
     for (int j = 0; j < it.nmax; ++j, ++tile) {
-      int pg[2] = {0, 0}, row[2] = {it.e.k0 + kTile * j, it.e.k0 + kTile * j + 64};
+      int page = 0, row = it.e.k0 + kKeys * j, flag = 0;
       if (p.page_table) {
-        const int pages = (it.e.kvlen + 63) >> 6;
-        if ((j & 15) == 0) {
-          const int i = 2 * j + lane;
-          win = i < pages ? p.page_table[(int64_t)it.e.b * p.pt_sb + i] : -2;
-        }
-        int flags = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int id = __shfl_sync(0xffffffffu, win, (2 * j + h) & 31);
-          const bool good = id >= 0 && id < p.num_blocks;
-          if (2 * j + h < pages) flags |= good ? 0 : 1 << h;
-          pg[h] = good ? id : max(p.num_blocks, 1);  // past the last page: reads as zeros
-          row[h] = 0;
-        }
-        if (lane == 0) {
-          if (flags) bounds();
-          ms.flags[tile % kFlagRing] = flags;
+        if ((j & 31) == 0)
+          win = j + lane < it.nmax ? p.page_table[(int64_t)it.e.b * p.pt_sb + j + lane] : 0;
+        page = __shfl_sync(0xffffffffu, win, j & 31);
+        row = 0;
+        if (page < 0 || page >= p.num_blocks) {
+          flag = 1;
+          page = max(p.num_blocks, 1);  // past the last page: reads as zeros
         }
       }
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         constexpr int kN[2] = {C::kNK, C::kNV};
-        const uint32_t full = smem_addr(&ms.full[(2 * tile + v) % kParts]);
-        for (int c = 0; c < kN[v]; ++c, ++n) {
-          const uint32_t slot = n % C::kRing;
-          int ok = 1;
-          if (lane == 0 && n >= C::kRing)
-            ok = wait_bar(smem_addr(&ms.empty[slot]), ((n / C::kRing) - 1) & 1, abort_flag,
-                          &g_kv_prefill_status);
-          if (!__shfl_sync(0xffffffffu, ok, 0)) return;
-          if (lane == 0 && c == 0) mbar_arrive_expect_tx(full, kN[v] * kStage);
-          __syncwarp();
-          if (lane < 2)
-            tma_load_5d(ring + slot * kStage + lane * (kStage / 2), v ? vm : km, 0,
-                        lane ? row[1] : row[0], c, it.hk, lane ? pg[1] : pg[0], full);
+        const uint32_t full = smem_addr(&ms.full[slot][v]);
+        int ok = 1;
+        if (lane == 0) {
+          if (tile >= C::kRing)
+            ok = wait_bar(smem_addr(&ms.empty[slot][v]), phase, abort_flag, &g_kv_prefill_status);
+          if (ok) {
+            if (v == 0) {
+              if (flag) bounds();
+              ms.flags[tile % kFlagRing] = flag;
+            }
+            mbar_arrive_expect_tx(full, kN[v] * kChunk);
+          }
         }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+        const int c = lane - (v ? C::kNK : 0);
+        if (c >= 0 && c < kN[v])
+          tma_load_5d(sbase + 2 * C::kQTile + slot * C::kKV + lane * kChunk, v ? vm : km, 0, row, c,
+                      it.hk, page, full);
+      }
+      if (++slot == C::kRing) {
+        slot = 0;
+        phase ^= 1;
       }
     }
   }
 }
 
-// Both products of both tiles, in one order: for each key tile j, tile A then
-// tile B: O += P V_j, then at once the tile's next S = Q K^T (key tile j + 1,
-// or key tile 0 of the next item), so that the tensor core has the other
-// tile's products to do while a softmax runs, across items too.
+// Where a query tile's products stand: item by item, key tile by key tile.
+template <int RING>
+struct Cursor {
+  Items items;
+  int n, nmax, j;        // key tiles of this query tile and of the item, the next one
+  uint32_t slot, phase;  // of key tile j
+  bool live;
+  __device__ Cursor(const Params& p, int t) : items(p), slot(0), phase(0) { next_item(p, t); }
+  __device__ void next_item(const Params& p, int t) {
+    Item it = {};
+    live = items.next(p, it);
+    n = t ? it.n[1] : it.n[0];
+    nmax = it.nmax;
+    j = 0;
+  }
+  __device__ void step(const Params& p, int t) {
+    skip(1);
+    if (++j == n) {
+      skip(nmax - n);  // key tiles of the other query tile
+      next_item(p, t);
+    }
+  }
+  __device__ void skip(int k) {
+    slot += k;
+    if (slot >= RING) {
+      slot -= RING;
+      phase ^= 1;
+    }
+  }
+};
+
+// The products of one query tile: S = Q K^T up to two key tiles ahead of
+// O += P V, each into the buffer that an earlier P has left.  A thread's
+// products complete in order, so the commit that announces the S of key tile
+// j + 2 also says that P V of tile j is done.
 //
-// What the tensor core waits for is this thread: every wait and every commit
-// costs it some 150 cycles, so there are few.  One commit per step (s_full)
-// says all: the products complete in order, so S of key tile j + 1 also means
-// that P V_j is done, and the softmax threads that see it free K and V.
+// Within an item the thread waits for the next K; a next item's first S is
+// made early only if its Q and K are there already.  (Waiting for them before
+// the last P V of an item could wait for ever: the ring's slots are freed
+// behind those products.)
 template <typename T, int DK, int DV>
-__device__ void mma_issuer(const Params& p, uint32_t sbase, uint32_t tmem, Misc& ms) {
+__device__ void mma_issuer(const Params& p, const int t, uint32_t sbase, uint32_t tmem, Misc& ms) {
   using C = Cfg<T, DK, DV>;
   volatile int* abort_flag = &ms.abort_flag;
-  const uint32_t ring = sbase + C::kQ;
-  const uint64_t dQ = sw128_desc(sbase, 16, 1024), dK = sw128_desc(ring, 16, 1024);
-  // V, MN-major: rows are keys, 64 columns to a 128-byte row; two chunks in
-  // consecutive stages are one operand whose column groups lie a stage apart
-  const uint64_t dV = sw128_desc(ring, kStage, 1024);
+  const uint32_t ring = sbase + 2 * C::kQTile;
+  const uint64_t dQ = sw128_desc(sbase + t * C::kQTile, 16, 1024), dK = sw128_desc(ring, 16, 1024);
+  // V, MN-major: rows are keys, 64 columns to a 128-byte row, column groups a
+  // chunk apart
+  const uint64_t dV = sw128_desc(ring + C::kNK * kChunk, kChunk, 1024);
+  constexpr uint32_t kC = kChunk >> 4, kT = C::kKV >> 4;
   const uint32_t q_lo = (uint32_t)dQ, k_lo = (uint32_t)dK, kk_hi = (uint32_t)(dK >> 32);
   const uint32_t v_lo = (uint32_t)dV, v_hi = (uint32_t)(dV >> 32);
-  constexpr uint32_t kS = kStage >> 4;
-  uint32_t tile = 0, slot = 0;  // key tiles before this one; ring slot of its K
-  uint32_t qloads[2] = {0, 0}, cnt[2] = {0, 0};
+  const uint32_t tS = tmem + kColS + kRows * t, tO = tmem + kColO + 128 * t;
   auto wait = [&](unsigned long long& bar, uint32_t parity) {
     return wait_bar(smem_addr(&bar), parity, abort_flag, &g_kv_prefill_status);
   };
-  auto wait_part = [&](uint32_t part) {
-    return wait(ms.full[part % kParts], (part / kParts) & 1);
-  };
-  auto wrap = [](uint32_t s) { return s >= C::kRing ? s - C::kRing : s; };
-  // S of tile t and key tile j of item `it`, whose K begins at ring slot s
-  auto qk = [&](const Item& it, int t, int j, uint32_t part, uint32_t s) {
-    if (j == 0) {
-      if (!wait(ms.q_full[t], qloads[t] & 1)) return false;
-      ++qloads[t];
-    }
-    if ((t == 0 || j >= it.n[0]) && !wait_part(part)) return false;  // tile A has waited for B
+  uint32_t qloads = 0, made = 0;  // query tiles used, S made
+  Cursor<C::kRing> ahead(p, t);
+  auto make_s = [&]() {  // its Q and K have landed
     tc_fence_after();
+    const uint32_t k0 = k_lo + ahead.slot * kT, buf = made & 1;
 #pragma unroll
-    for (int c = 0; c < C::kNK; ++c) {
-      const uint32_t a = q_lo + (uint32_t)(t * C::kNK + c) * kS;
-      const uint32_t b = k_lo + wrap(s + c) * kS;
+    for (int c = 0; c < C::kNK; ++c)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        mma_ss(tmem + kColS + kTile * t, a + 2 * k, kk_hi, b + 2 * k, kk_hi, C::idesc(128, false),
-               (c | k) != 0);
-    }
-    commit(smem_addr(&ms.s_full[t]));
-    if (j + 1 == it.n[t]) commit(smem_addr(&ms.q_empty[t]));
-    return true;
+        mma_ss(tS + kKeys * buf, q_lo + 2 * c * kC + 2 * k, kk_hi, k0 + c * kC + 2 * k, kk_hi,
+               C::idesc(kKeys, false), (c | k) != 0);
+    commit(smem_addr(&ms.s_full[t][buf]));
+    if (ahead.j + 1 == ahead.n) commit(smem_addr(&ms.q_empty[t]));
+    if (ahead.j == 0) ++qloads;
+    ++made;
+    ahead.step(p, t);
   };
-  Items items(p);
-  Item it, nx;
-  if (!items.next(p, it)) return;
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-    if (it.n[t] > 0 && !qk(it, t, 0, 0, 0)) return;
-  for (bool more = true; more;) {
-    more = items.next(p, nx);
-    for (int j = 0; j < it.nmax; ++j, ++tile) {
-      const uint32_t sv = wrap(slot + C::kNK), sn = wrap(sv + C::kNV);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (j < it.n[t]) {
-          if ((t == 0 || j >= it.n[0]) && !wait_part(2 * tile + 1)) return;
-          if (!wait(ms.p_full[t], cnt[t] & 1)) return;
-          ++cnt[t];
-          tc_fence_after();
-          const uint32_t pa = tmem + kColS + kTile * t;
-          const uint32_t dO = tmem + kColO + kTile * t;
-          if (C::kNV == 1 || sv + 1 < C::kRing) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_ts(dO, pa + 8 * k, v_lo + sv * kS + 128 * k, v_hi, C::idesc(DV, true),
-                     (j | k) != 0);
-          } else {  // the chunks lie at the ring's end and its beginning
-#pragma unroll
-            for (int c = 0; c < C::kNV; ++c)
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_ts(dO + 64 * c, pa + 8 * k, v_lo + wrap(sv + c) * kS + 128 * k, v_hi,
-                       C::idesc(64, true), (j | k) != 0);
-          }
-          if (j + 1 < it.n[t]) {
-            if (!qk(it, t, j + 1, 2 * tile + 2, sn)) return;
-          } else {
-            commit(smem_addr(&ms.o_full[t]));
-          }
-        }
-        // the ring holds this item's last V and the next item's first K
-        if (j + 1 == it.nmax && more && nx.n[t] > 0 && !qk(nx, t, 0, 2 * tile + 2, sn)) return;
-      }
-      slot = sn;
+  auto wait_s = [&]() {
+    if (ahead.j == 0 && !wait(ms.q_full[t], qloads & 1)) return false;
+    return wait(ms.full[ahead.slot][0], ahead.phase);
+  };
+  Cursor<C::kRing> at(p, t);
+  for (uint32_t cnt = 0; at.live; ++cnt) {
+    const int buf = cnt & 1;
+    if (made == cnt) {
+      if (!wait_s()) return;
+      make_s();
     }
-    it = nx;
+    bool early = false;
+    if (made == cnt + 1 && ahead.live) {
+      if (ahead.j > 0) {
+        if (!wait_s()) return;
+        make_s();
+      } else {
+        early = true;
+      }
+    }
+    if (!wait(ms.full[at.slot][1], at.phase)) return;
+    const uint32_t pbar = smem_addr(&ms.p_full[t][buf]), parity = (cnt >> 1) & 1;
+    if (early) {
+      const long long t0 = clock64();
+      while (!mbar_test(pbar, parity)) {
+        if (mbar_test(smem_addr(&ms.q_full[t]), qloads & 1) &&
+            mbar_test(smem_addr(&ms.full[ahead.slot][0]), ahead.phase)) {
+          make_s();
+          break;
+        }
+        if (*abort_flag || clock64() - t0 > kTimeoutCycles) break;
+      }
+    }
+    if (!wait(ms.p_full[t][buf], parity)) return;
+    tc_fence_after();
+    const uint32_t v0 = v_lo + at.slot * kT;
+#pragma unroll
+    for (int k = 0; k < kKeys / 16; ++k)
+      mma_ts(tO, tS + kKeys * buf + 8 * k, v0 + 128 * k, v_hi, C::idesc(DV, true),
+             (at.j | k) != 0);
+    if (at.j + 2 == at.n) commit(smem_addr(&ms.o_last[t]));
+    if (at.j + 1 == at.n) commit(smem_addr(&ms.o_full[t]));
+    at.step(p, t);
   }
 }
 
 template <typename T, int DK, int DV>
-__device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, Misc& ms) {
+__device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t tmem, Misc& ms) {
   using C = Cfg<T, DK, DV>;
   volatile int* abort_flag = &ms.abort_flag;
   const int w = (int)(threadIdx.x >> 5) & 3;
   const int row = 32 * w + (int)(threadIdx.x & 31);  // this thread's row and TMEM lane
   const uint32_t lane_base = (uint32_t)(32 * w) << 16;
-  const uint32_t tS = tmem + lane_base + kColS + kTile * t;
-  const uint32_t tO = tmem + lane_base + kColO + kTile * t;
-  const uint32_t ring = sbase + C::kQ;
+  const uint32_t tS = tmem + lane_base + kColS + kRows * t;
+  const uint32_t tO = tmem + lane_base + kColO + 128 * t;
   const int my_tok = row / p.gg, my_head = row - my_tok * p.gg;
-  uint32_t cnt = 0, tiles = 0, done = 0;
-  // frees the stages of a part whose last reader is this tile
+  uint32_t cnt = 0, tiles = 0, done = 0, pairs = 0;  // pairs: items of two key tiles or more
+  const bool leader = (threadIdx.x & 127) == 0;
+  // this query tile needs K (v = 0) or V of a key tile no longer
   auto release = [&](uint32_t tile, int v) {
-    if ((threadIdx.x & 127) == 0) {
-      const uint32_t s = tile * C::kSPT + (v ? C::kNK : 0);
-      for (int c = 0; c < (v ? C::kNV : C::kNK); ++c)
-        arrive(smem_addr(&ms.empty[(s + c) % C::kRing]));
-    }
+    if (leader) arrive(smem_addr(&ms.empty[tile % C::kRing][v]));
   };
   auto wait = [&](unsigned long long& bar, uint32_t parity) {
     const bool ok = wait_bar(smem_addr(&bar), parity, abort_flag, &g_kv_prefill_status);
@@ -422,51 +447,52 @@ __device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, M
     const int n = t ? it.n[1] : it.n[0];
     float m = -INFINITY, l = 0.f, lx = 0.f;  // maximum; sums of the 16-bit and the f32 weights
     for (int j = 0; j < n; ++j, ++cnt) {
-      if (!wait(ms.s_full[t], cnt & 1)) return;
+      const int buf = cnt & 1;
+      const uint32_t ts = tS + kKeys * buf;
+      if (!wait(ms.s_full[t][buf], (cnt >> 1) & 1)) return;
       tc_fence_after();
-      // this S is done, and with it the P V before it
-      if (t == 1 || j >= it.n[1]) release(tiles + j, 0);
-      if (j > 0 && (t == 1 || j - 1 >= it.n[1])) release(tiles + j - 1, 1);
-      float x[128];
+      // this S is done, and with it the P V of two key tiles before
+      release(tiles + j, 0);
+      if (j > 1) release(tiles + j - 2, 1);
+      float x[kKeys];
       {
-        uint32_t r[4][32];
-        tmem_ld32(tS, r[0]);
-        tmem_ld32(tS + 32, r[1]);
-        tmem_ld32(tS + 64, r[2]);
-        tmem_ld32(tS + 96, r[3]);
+        uint32_t r[2][32];
+        tmem_ld32(ts, r[0]);
+        tmem_ld32(ts + 32, r[1]);
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 128; ++k) x[k] = __uint_as_float(r[k >> 5][k & 31]);
+        for (int k = 0; k < kKeys; ++k) x[k] = __uint_as_float(r[k >> 5][k & 31]);
       }
       if (p.negate) {
 #pragma unroll
-        for (int k = 0; k < 128; ++k) x[k] = -x[k];
+        for (int k = 0; k < kKeys; ++k) x[k] = -x[k];
       }
-      const int nv = limit - kTile * j;
-      const int flags = p.page_table ? ms.flags[(tiles + j) % kFlagRing] : 0;
-      if (__any_sync(0xffffffffu, nv < kTile) || flags) {
+      int nv = limit - kKeys * j;
+      if (p.page_table && ms.flags[(tiles + j) % kFlagRing]) nv = 0;  // a bad page
+      const bool masked = __any_sync(0xffffffffu, nv < kKeys);
+      if (masked) {
 #pragma unroll
-        for (int k = 0; k < 128; ++k)
-          x[k] = k < nv && !(flags >> (k >> 6) & 1) ? x[k] : -INFINITY;
+        for (int k = 0; k < kKeys; ++k) x[k] = k < nv ? x[k] : -INFINITY;
       }
       float mxs[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         mxs[i] = fmaxf(x[2 * i], x[2 * i + 1]);
 #pragma unroll
-        for (int k = 8 + 2 * i; k < 128; k += 8) mxs[i] = max3(mxs[i], x[k], x[k + 1]);
+        for (int k = 8 + 2 * i; k < kKeys; k += 8) mxs[i] = max3(mxs[i], x[k], x[k + 1]);
       }
       const float mx = fmaxf(max3(mxs[0], mxs[1], mxs[2]), mxs[3]) * p.scale_log2;
-      float factor = 1.f;
-      bool resc = false;
-      if (m == -INFINITY) {
-        m = mx;
-      } else if (mx > m + kRescaleThreshold) {
-        factor = ex2(m - mx);
-        m = mx;
-        resc = true;
-      }
-      if (__any_sync(0xffffffffu, resc)) {  // O as the previous P V left it
+      const bool resc = mx > m + kRescaleThreshold && m != -INFINITY;
+      if (m == -INFINITY) m = mx;
+      if (__any_sync(0xffffffffu, resc)) {
+        // O as the P V before this one leaves it: the next S says that it is
+        // done, before an item's last key tile a barrier of its own
+        if (!(j + 1 < n ? wait(ms.s_full[t][buf ^ 1], ((cnt + 1) >> 1) & 1)
+                        : wait(ms.o_last[t], pairs & 1)))
+          return;
+        tc_fence_after();
+        const float factor = resc ? ex2(m - mx) : 1.f;
+        if (resc) m = mx;
         l *= factor;
         lx *= factor;
 #pragma unroll
@@ -480,58 +506,69 @@ __device__ void softmax(const Params& p, int t, uint32_t sbase, uint32_t tmem, M
         }
         tmem_wait_st();
       }
+      const int left = it.e.kvlen - kKeys * j;
+      if (left < kKeys) {
+        // behind the request's last key stand other rows or stale ones; a
+        // weight of 0 does not stop an infinity or a NaN there, so they are
+        // cleared before P V reads them
+        const uint32_t tile = tiles + j, slot = tile % C::kRing;
+        if (!wait(ms.full[slot][1], (tile / C::kRing) & 1)) return;
+        if (row >= left && row < kKeys) {
+          const uint32_t v = sbase + 2 * C::kQTile + slot * C::kKV + C::kNK * kChunk + row * 128;
+#pragma unroll
+          for (int i = 0; i < 8 * C::kNV; ++i)
+            st_shared_v4(v + (i >> 3) * kChunk + 16 * (i & 7), 0, 0, 0, 0);
+        }
+        fence_async_smem();
+      }
       const float mu = m == -INFINITY ? 0.f : m;
       const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
       uint64_t s16 = f2_pack(0.f, 0.f), s32 = f2_pack(0.f, 0.f);
+      uint32_t pk[32];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          float e0, e1;
-          f2_unpack(f2_fma(f2_pack(x[64 * h + 2 * k], x[64 * h + 2 * k + 1]), sc, nm), e0, e1);
-          e0 = ex2(e0);
-          e1 = ex2(e1);
-          pk[k] = T::pack(e0, e1);
-          const float2 e = T::unpack(pk[k]);
-          s32 = f2_add(s32, f2_pack(e0, e1));
-          s16 = f2_add(s16, f2_pack(e.x, e.y));
-        }
-        tmem_st32(tS + 32 * h, pk);  // over this row's own scores: they are in registers
+      for (int k = 0; k < 32; ++k) {
+        float e0, e1;
+        f2_unpack(f2_fma(f2_pack(x[2 * k], x[2 * k + 1]), sc, nm), e0, e1);
+        e0 = ex2(e0);
+        e1 = ex2(e1);
+        pk[k] = T::pack(e0, e1);
+        const float2 e = T::unpack(pk[k]);
+        s32 = f2_add(s32, f2_pack(e0, e1));
+        s16 = f2_add(s16, f2_pack(e.x, e.y));
       }
+      tmem_st32(ts, pk);  // over this row's own scores: they are in registers
       float a, b;
       f2_unpack(s16, a, b);
       l += a + b;
       f2_unpack(s32, a, b);
       lx += a + b;
-      const int left = it.e.kvlen - kTile * j;
-      if (left < kTile) {
-        // behind the request's last key stand other rows or stale ones; a
-        // weight of 0 does not stop an infinity or a NaN there, so they are
-        // cleared before P V reads them
-        const uint32_t sv = (tiles + j) * C::kSPT + C::kNK, part = 2 * (tiles + j) + 1;
-        if (!wait(ms.full[part % kParts], (part / kParts) & 1)) return;
-#pragma unroll
-        for (int c = 0; c < C::kNV; ++c) {
-          const uint32_t slot = (sv + c) % C::kRing;
-          if (row >= left)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              st_shared_v4(ring + slot * kStage + row * 128 + 16 * i, 0, 0, 0, 0);
-        }
-        fence_async_smem();
-      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) arrive(smem_addr(&ms.p_full[t]));
+      if ((threadIdx.x & 31) == 0) arrive(smem_addr(&ms.p_full[t][buf]));
     }
     if (n > 0) {
       if (!wait(ms.o_full[t], done & 1)) return;
       ++done;
       tc_fence_after();
-      if (t == 1 || n > it.n[1]) release(tiles + n - 1, 1);
+      if (n > 1) {
+        release(tiles + n - 2, 1);
+        ++pairs;
+      }
+      release(tiles + n - 1, 1);
     }
+    if (leader) {  // key tiles that only the other query tile reads, as they come
+      for (int j = n; j < it.nmax; ++j) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t tile = tiles + j;
+          if (wait_bar(smem_addr(&ms.full[tile % C::kRing][v]), (tile / C::kRing) & 1, abort_flag,
+                       &g_kv_prefill_status))
+            release(tile, v);
+        }
+      }
+    }
+    __syncwarp();
     tiles += it.nmax;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : NAN);
     const int64_t orow = (int64_t)(it.e.q0 + tok) * p.o_st + (int64_t)(it.hk * p.g + head) * p.o_sh;
@@ -583,17 +620,22 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant_
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
-  Misc& ms = *reinterpret_cast<Misc*>(smem + C::kQ + C::kRing * kStage);
+  Misc& ms = *reinterpret_cast<Misc*>(smem + 2 * C::kQTile + C::kRing * C::kKV);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kParts; ++s) mbar_init(smem_addr(&ms.full[s]), 1);
-    for (int s = 0; s < C::kRing; ++s) mbar_init(smem_addr(&ms.empty[s]), 1);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_addr(&ms.q_full[t]), 1);
-      mbar_init(smem_addr(&ms.q_empty[t]), 1);
-      mbar_init(smem_addr(&ms.s_full[t]), 1);
-      mbar_init(smem_addr(&ms.p_full[t]), 4);
-      mbar_init(smem_addr(&ms.o_full[t]), 1);
+    for (int i = 0; i < 2; ++i) {
+      for (int s = 0; s < C::kRing; ++s) {
+        mbar_init(smem_addr(&ms.full[s][i]), 1);
+        mbar_init(smem_addr(&ms.empty[s][i]), 2);
+      }
+      mbar_init(smem_addr(&ms.q_full[i]), 1);
+      mbar_init(smem_addr(&ms.q_empty[i]), 1);
+      mbar_init(smem_addr(&ms.o_last[i]), 1);
+      mbar_init(smem_addr(&ms.o_full[i]), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_addr(&ms.s_full[i][b]), 1);
+        mbar_init(smem_addr(&ms.p_full[i][b]), 4);
+      }
     }
     ms.abort_flag = 0;
     fence_mbar_init();
@@ -616,17 +658,13 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant_
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the list of items
 
   if (warp >= kWarpSm0) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     softmax<T, DK, DV>(p, (warp - kWarpSm0) >> 2, sbase, tmem, ms);
+  } else if (warp < kWarpProd) {
+    if (lane == 0) mma_issuer<T, DK, DV>(p, warp - kWarpMma, sbase, tmem, ms);
+  } else if (warp == kWarpProd) {
+    producer<T, DK, DV>(p, &km, &vm, sbase, ms);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == kWarpMma) {
-      if (lane == 0) mma_issuer<T, DK, DV>(p, sbase, tmem, ms);
-    } else if (warp == kWarpProd) {
-      producer<T, DK, DV>(p, &km, &vm, sbase, ms);
-    } else if (warp == kWarpQ) {
-      q_producer<T, DK, DV>(p, &qm, sbase, ms);
-    }
+    q_producer<T, DK, DV>(p, &qm, sbase, ms);
   }
   __syncwarp();
   tc_fence_before();
@@ -653,14 +691,14 @@ __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, E
   for (int b = threadIdx.x; b < p.B; b += 1024) {
     Entry e;
     request(p, b, e);
-    most = max(most, (e.kvlen + kTile - 1) / kTile);
+    most = max(most, (e.kvlen + kKeys - 1) / kKeys);
   }
   if (most) atomicMax(&top, most);
   __syncthreads();
   int shift = 0;
   while ((top >> shift) >= kBuckets) ++shift;
   auto bucket = [&](const Entry& e, int t0) {  // 0 for the longest
-    const int tiles = (limit_of(p, e, min(t0 + tb, e.qlen) - 1) + kTile - 1) / kTile;
+    const int tiles = (limit_of(p, e, min(t0 + tb, e.qlen) - 1) + kKeys - 1) / kKeys;
     return kBuckets - 1 - (tiles >> shift);
   };
   for (int b = warp; b < p.B; b += 32) {
@@ -715,9 +753,9 @@ struct Shape {
 Shape shape(const KvPrefillProblem& p) {
   Shape s;
   s.g = p.Hq / p.kv.Hkv;
-  s.gg = s.g < kTile ? s.g : kTile;
+  s.gg = s.g < kRows ? s.g : kRows;
   s.groups = (s.g + s.gg - 1) / s.gg;
-  s.tpt = kTile / s.gg;
+  s.tpt = kRows / s.gg;
   s.entries = (int64_t)p.T / (2 * s.tpt) + p.B;
   return s;
 }
