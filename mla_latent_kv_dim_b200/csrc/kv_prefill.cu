@@ -12,10 +12,11 @@
 //    key head (row = token * g + head), so that grouped heads share every
 //    key and value tile and few tokens still fill the rows;
 //  * a work item is two such tiles A and B of consecutive tokens, which share
-//    the key tiles of 64 keys.  Each has an issuing thread, a softmax
-//    warpgroup, O in TMEM and two S buffers of 64 columns there: while the
-//    softmax works on one S the tensor core fills the other, so neither waits
-//    out the other's latency.  P goes over its own S as 16-bit pairs, the A
+//    the key tiles of 64 keys.  Each has a softmax warpgroup, O in TMEM and
+//    two S buffers of 64 columns there: while the softmax works on one S the
+//    tensor core fills the other, so neither waits out the other's latency.
+//    Three threads issue the products (Q K^T of A, of B, and both P V), so
+//    that the waits of one pass while the others feed the tensor core.  P goes over its own S as 16-bit pairs, the A
 //    operand from TMEM: 2 x (128 + Dv) of the 512 columns in all.  (With one S
 //    of 128 keys, Q K^T had to wait for P V, P V for the softmax and the
 //    softmax for Q K^T: 4450 cycles for 128 keys of both tiles against 2048 of
@@ -46,9 +47,10 @@ constexpr int kRows = 128;    // rows of a query tile
 constexpr int kKeys = 64;     // keys of a key tile
 constexpr int kChunk = 8192;  // 64 keys x 64 columns
 constexpr int kThreads = 384;
-// Warps 0 and 1 issue the products of query tiles A and B, 4-7 and 8-11 are
-// their softmax warpgroups; 2 loads key tiles, 3 query tiles.
-constexpr int kWarpMma = 0, kWarpProd = 2, kWarpSm0 = 4;
+// Warps 0 and 1 load the query tiles A and B and issue their Q K^T, 2 issues
+// P V of both, 3 loads key tiles; 4-7 and 8-11 are the softmax warpgroups of A
+// and B.
+constexpr int kWarpQK = 0, kWarpPV = 2, kWarpProd = 3, kWarpSm0 = 4;
 constexpr int kMaxRing = 12;   // key tiles
 constexpr int kFlagRing = 16;  // key tiles whose page flags are kept (> kMaxRing + 2)
 constexpr int kSmemBytes = 232448;
@@ -192,7 +194,7 @@ struct Cfg {
   static constexpr int kRing0 = (kSmemBytes - 1024 - kMiscBytes - 2 * kQTile) / kKV;
   static constexpr int kRing = kRing0 < kMaxRing ? kRing0 : kMaxRing;
   static constexpr int kSmem = 1024 + 2 * kQTile + kRing * kKV + kMiscBytes;
-  // Q K^T runs two key tiles ahead of P V
+  // Q K^T runs up to two key tiles ahead of P V
   static_assert(kSmem <= kSmemBytes && kRing >= 3, "shared memory");
   static constexpr uint32_t idesc(int n, bool b_mn) {
     return (1u << 4) | ((uint32_t)T::kFormat << 7) | ((uint32_t)T::kFormat << 10) |
@@ -201,45 +203,17 @@ struct Cfg {
 };
 
 struct Misc {
-  // per ring slot, K and V: landed; no longer needed by either query tile
+  // per ring slot: K and V landed; K no longer needed by either softmax
+  // (their S are made), V no longer by P V
   unsigned long long full[kMaxRing][2], empty[kMaxRing][2];
   unsigned long long q_full[2], q_empty[2];
-  unsigned long long o_last[2], o_full[2];  // the item's last P V but one, its last
-  unsigned long long s_full[2][2], p_full[2][2];  // per query tile and S buffer
+  // per query tile and S buffer: S made, P stored, P V done
+  unsigned long long s_full[2][2], p_full[2][2], pv_done[2][2];
   int flags[kFlagRing];
   uint32_t tmem;
   int abort_flag;
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc shared memory");
-
-// Query tiles: each as soon as the last Q K^T of the tile before it is done.
-template <typename T, int DK, int DV>
-__device__ void q_producer(const Params& p, const CUtensorMap* qm, uint32_t sbase, Misc& ms) {
-  using C = Cfg<T, DK, DV>;
-  const int lane = threadIdx.x & 31;
-  volatile int* abort_flag = &ms.abort_flag;
-  Items items(p);
-  Item it;
-  uint32_t loads[2] = {0, 0};
-  while (items.next(p, it)) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint32_t qf = smem_addr(&ms.q_full[t]);
-      int ok = 1;
-      if (lane == 0) {
-        if (loads[t] > 0)
-          ok = wait_bar(smem_addr(&ms.q_empty[t]), (loads[t] - 1) & 1, abort_flag,
-                        &g_kv_prefill_status);
-        if (ok) mbar_arrive_expect_tx(qf, C::kNK * p.gg * p.tpt * 128);
-      }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) return;
-      ++loads[t];
-      if (lane < C::kNK)
-        tma_load_5d(sbase + t * C::kQTile + lane * kRows * 128, qm, 0, it.rg * p.gg,
-                    it.e.q0 + it.e.t0 + t * p.tpt, lane, it.hk, qf);
-    }
-  }
-}
 
 // Key tiles: a chunk from a lane of its own, because a thread's copies land
 // one after another.
@@ -297,122 +271,111 @@ __device__ void producer(const Params& p, const CUtensorMap* km, const CUtensorM
   }
 }
 
-// Where a query tile's products stand: item by item, key tile by key tile.
-template <int RING>
-struct Cursor {
-  Items items;
-  int n, nmax, j;        // key tiles of this query tile and of the item, the next one
-  uint32_t slot, phase;  // of key tile j
-  bool live;
-  __device__ Cursor(const Params& p, int t) : items(p), slot(0), phase(0) { next_item(p, t); }
-  __device__ void next_item(const Params& p, int t) {
-    Item it = {};
-    live = items.next(p, it);
-    n = t ? it.n[1] : it.n[0];
-    nmax = it.nmax;
-    j = 0;
-  }
-  __device__ void step(const Params& p, int t) {
-    skip(1);
-    if (++j == n) {
-      skip(nmax - n);  // key tiles of the other query tile
-      next_item(p, t);
+// Query tile t: its loads, and S = Q K^T of each key tile into the S buffer
+// whose P V is done, two key tiles ahead of P V.
+template <typename T, int DK, int DV>
+__device__ void qk_issuer(const Params& p, const int t, const CUtensorMap* qm, uint32_t sbase,
+                          uint32_t tmem, Misc& ms) {
+  using C = Cfg<T, DK, DV>;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &ms.abort_flag;
+  const uint64_t dQ = sw128_desc(sbase + t * C::kQTile, 16, 1024);
+  const uint64_t dK = sw128_desc(sbase + 2 * C::kQTile, 16, 1024);
+  constexpr uint32_t kC = kChunk >> 4, kT = C::kKV >> 4;
+  const uint32_t q_lo = (uint32_t)dQ, k_lo = (uint32_t)dK, hi = (uint32_t)(dK >> 32);
+  const uint32_t tS = tmem + kColS + kRows * t;
+  const uint32_t q_full = smem_addr(&ms.q_full[t]), q_empty = smem_addr(&ms.q_empty[t]);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return wait_bar(bar, parity, abort_flag, &g_kv_prefill_status);
+  };
+  Items items(p);
+  Item it;
+  uint32_t cnt = 0, slot = 0, phase = 0;
+  for (uint32_t i = 0; items.next(p, it); ++i) {
+    const int n = t ? it.n[1] : it.n[0];
+    int ok = 1;
+    if (lane == 0) {
+      ok = i == 0 || wait(q_empty, (i - 1) & 1);
+      if (ok) mbar_arrive_expect_tx(q_full, C::kNK * p.gg * p.tpt * 128);
     }
-  }
-  __device__ void skip(int k) {
-    slot += k;
-    if (slot >= RING) {
-      slot -= RING;
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+    if (lane < C::kNK)  // a thread's copies land one after another
+      tma_load_5d(sbase + t * C::kQTile + lane * kRows * 128, qm, 0, it.rg * p.gg,
+                  it.e.q0 + it.e.t0 + t * p.tpt, lane, it.hk, q_full);
+    __syncwarp();
+    if (lane == 0) {
+      ok = wait(q_full, i & 1);
+      for (int j = 0; ok && j < n; ++j, ++cnt) {
+        const uint32_t buf = cnt & 1;
+        ok = wait(smem_addr(&ms.full[slot][0]), phase) &&
+             (cnt < 2 || wait(smem_addr(&ms.pv_done[t][buf]), ((cnt - 2) >> 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t k0 = k_lo + slot * kT, dS = tS + kKeys * buf;
+#pragma unroll
+        for (int c = 0; c < C::kNK; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss(dS, q_lo + 2 * c * kC + 2 * k, hi, k0 + c * kC + 2 * k, hi,
+                   C::idesc(kKeys, false), (c | k) != 0);
+        commit(smem_addr(&ms.s_full[t][buf]));
+        if (++slot == C::kRing) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
+      if (ok) commit(q_empty);
+    }
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+    slot = __shfl_sync(0xffffffffu, slot, 0) + (it.nmax - n);  // the other query tile's
+    phase = __shfl_sync(0xffffffffu, phase, 0);
+    if (slot >= C::kRing) {
+      slot -= C::kRing;
       phase ^= 1;
     }
+    cnt = __shfl_sync(0xffffffffu, cnt, 0);
   }
-};
+}
 
-// The products of one query tile: S = Q K^T up to two key tiles ahead of
-// O += P V, each into the buffer that an earlier P has left.  A thread's
-// products complete in order, so the commit that announces the S of key tile
-// j + 2 also says that P V of tile j is done.
-//
-// Within an item the thread waits for the next K; a next item's first S is
-// made early only if its Q and K are there already.  (Waiting for them before
-// the last P V of an item could wait for ever: the ring's slots are freed
-// behind those products.)
+// O += P V of both query tiles, key tile by key tile.
 template <typename T, int DK, int DV>
-__device__ void mma_issuer(const Params& p, const int t, uint32_t sbase, uint32_t tmem, Misc& ms) {
+__device__ void pv_issuer(const Params& p, uint32_t sbase, uint32_t tmem, Misc& ms) {
   using C = Cfg<T, DK, DV>;
   volatile int* abort_flag = &ms.abort_flag;
-  const uint32_t ring = sbase + 2 * C::kQTile;
-  const uint64_t dQ = sw128_desc(sbase + t * C::kQTile, 16, 1024), dK = sw128_desc(ring, 16, 1024);
   // V, MN-major: rows are keys, 64 columns to a 128-byte row, column groups a
   // chunk apart
-  const uint64_t dV = sw128_desc(ring + C::kNK * kChunk, kChunk, 1024);
-  constexpr uint32_t kC = kChunk >> 4, kT = C::kKV >> 4;
-  const uint32_t q_lo = (uint32_t)dQ, k_lo = (uint32_t)dK, kk_hi = (uint32_t)(dK >> 32);
+  const uint64_t dV = sw128_desc(sbase + 2 * C::kQTile + C::kNK * kChunk, kChunk, 1024);
+  constexpr uint32_t kT = C::kKV >> 4;
   const uint32_t v_lo = (uint32_t)dV, v_hi = (uint32_t)(dV >> 32);
-  const uint32_t tS = tmem + kColS + kRows * t, tO = tmem + kColO + 128 * t;
-  auto wait = [&](unsigned long long& bar, uint32_t parity) {
-    return wait_bar(smem_addr(&bar), parity, abort_flag, &g_kv_prefill_status);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return wait_bar(bar, parity, abort_flag, &g_kv_prefill_status);
   };
-  uint32_t qloads = 0, made = 0;  // query tiles used, S made
-  Cursor<C::kRing> ahead(p, t);
-  auto make_s = [&]() {  // its Q and K have landed
-    tc_fence_after();
-    const uint32_t k0 = k_lo + ahead.slot * kT, buf = made & 1;
+  Items items(p);
+  Item it;
+  uint32_t cnt[2] = {0, 0}, slot = 0, phase = 0;
+  while (items.next(p, it)) {
+    for (int j = 0; j < it.nmax; ++j) {
+      if (!wait(smem_addr(&ms.full[slot][1]), phase)) return;
+      const uint32_t v0 = v_lo + slot * kT;
 #pragma unroll
-    for (int c = 0; c < C::kNK; ++c)
+      for (int t = 0; t < 2; ++t) {
+        if (j >= it.n[t]) continue;
+        const uint32_t buf = cnt[t] & 1;
+        if (!wait(smem_addr(&ms.p_full[t][buf]), (cnt[t] >> 1) & 1)) return;
+        ++cnt[t];
+        tc_fence_after();
+        const uint32_t pS = tmem + kColS + kRows * t + kKeys * buf, tO = tmem + kColO + 128 * t;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mma_ss(tS + kKeys * buf, q_lo + 2 * c * kC + 2 * k, kk_hi, k0 + c * kC + 2 * k, kk_hi,
-               C::idesc(kKeys, false), (c | k) != 0);
-    commit(smem_addr(&ms.s_full[t][buf]));
-    if (ahead.j + 1 == ahead.n) commit(smem_addr(&ms.q_empty[t]));
-    if (ahead.j == 0) ++qloads;
-    ++made;
-    ahead.step(p, t);
-  };
-  auto wait_s = [&]() {
-    if (ahead.j == 0 && !wait(ms.q_full[t], qloads & 1)) return false;
-    return wait(ms.full[ahead.slot][0], ahead.phase);
-  };
-  Cursor<C::kRing> at(p, t);
-  for (uint32_t cnt = 0; at.live; ++cnt) {
-    const int buf = cnt & 1;
-    if (made == cnt) {
-      if (!wait_s()) return;
-      make_s();
-    }
-    bool early = false;
-    if (made == cnt + 1 && ahead.live) {
-      if (ahead.j > 0) {
-        if (!wait_s()) return;
-        make_s();
-      } else {
-        early = true;
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_ts(tO, pS + 8 * k, v0 + 128 * k, v_hi, C::idesc(DV, true), (j | k) != 0);
+        commit(smem_addr(&ms.pv_done[t][buf]));
+      }
+      commit(smem_addr(&ms.empty[slot][1]));
+      if (++slot == C::kRing) {
+        slot = 0;
+        phase ^= 1;
       }
     }
-    if (!wait(ms.full[at.slot][1], at.phase)) return;
-    const uint32_t pbar = smem_addr(&ms.p_full[t][buf]), parity = (cnt >> 1) & 1;
-    if (early) {
-      const long long t0 = clock64();
-      while (!mbar_test(pbar, parity)) {
-        if (mbar_test(smem_addr(&ms.q_full[t]), qloads & 1) &&
-            mbar_test(smem_addr(&ms.full[ahead.slot][0]), ahead.phase)) {
-          make_s();
-          break;
-        }
-        if (*abort_flag || clock64() - t0 > kTimeoutCycles) break;
-      }
-    }
-    if (!wait(ms.p_full[t][buf], parity)) return;
-    tc_fence_after();
-    const uint32_t v0 = v_lo + at.slot * kT;
-#pragma unroll
-    for (int k = 0; k < kKeys / 16; ++k)
-      mma_ts(tO, tS + kKeys * buf + 8 * k, v0 + 128 * k, v_hi, C::idesc(DV, true),
-             (at.j | k) != 0);
-    if (at.j + 2 == at.n) commit(smem_addr(&ms.o_last[t]));
-    if (at.j + 1 == at.n) commit(smem_addr(&ms.o_full[t]));
-    at.step(p, t);
   }
 }
 
@@ -426,11 +389,11 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
   const uint32_t tS = tmem + lane_base + kColS + kRows * t;
   const uint32_t tO = tmem + lane_base + kColO + 128 * t;
   const int my_tok = row / p.gg, my_head = row - my_tok * p.gg;
-  uint32_t cnt = 0, tiles = 0, done = 0, pairs = 0;  // pairs: items of two key tiles or more
+  uint32_t cnt = 0, tiles = 0;
   const bool leader = (threadIdx.x & 127) == 0;
-  // this query tile needs K (v = 0) or V of a key tile no longer
-  auto release = [&](uint32_t tile, int v) {
-    if (leader) arrive(smem_addr(&ms.empty[tile % C::kRing][v]));
+  // this query tile needs the key tile's K no longer; the other says so too
+  auto release = [&](uint32_t tile) {
+    if (leader) arrive(smem_addr(&ms.empty[tile % C::kRing][0]));
   };
   auto wait = [&](unsigned long long& bar, uint32_t parity) {
     const bool ok = wait_bar(smem_addr(&bar), parity, abort_flag, &g_kv_prefill_status);
@@ -451,9 +414,7 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
       const uint32_t ts = tS + kKeys * buf;
       if (!wait(ms.s_full[t][buf], (cnt >> 1) & 1)) return;
       tc_fence_after();
-      // this S is done, and with it the P V of two key tiles before
-      release(tiles + j, 0);
-      if (j > 1) release(tiles + j - 2, 1);
+      release(tiles + j);
       float x[kKeys];
       {
         uint32_t r[2][32];
@@ -485,11 +446,8 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
       const bool resc = mx > m + kRescaleThreshold && m != -INFINITY;
       if (m == -INFINITY) m = mx;
       if (__any_sync(0xffffffffu, resc)) {
-        // O as the P V before this one leaves it: the next S says that it is
-        // done, before an item's last key tile a barrier of its own
-        if (!(j + 1 < n ? wait(ms.s_full[t][buf ^ 1], ((cnt + 1) >> 1) & 1)
-                        : wait(ms.o_last[t], pairs & 1)))
-          return;
+        // O as the P V before this one leaves it (no maximum before the first)
+        if (!wait(ms.pv_done[t][buf ^ 1], ((cnt - 1) >> 1) & 1)) return;
         tc_fence_after();
         const float factor = resc ? ex2(m - mx) : 1.f;
         if (resc) m = mx;
@@ -548,24 +506,15 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
       if ((threadIdx.x & 31) == 0) arrive(smem_addr(&ms.p_full[t][buf]));
     }
     if (n > 0) {
-      if (!wait(ms.o_full[t], done & 1)) return;
-      ++done;
+      if (!wait(ms.pv_done[t][(cnt - 1) & 1], ((cnt - 1) >> 1) & 1)) return;
       tc_fence_after();
-      if (n > 1) {
-        release(tiles + n - 2, 1);
-        ++pairs;
-      }
-      release(tiles + n - 1, 1);
     }
     if (leader) {  // key tiles that only the other query tile reads, as they come
       for (int j = n; j < it.nmax; ++j) {
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint32_t tile = tiles + j;
-          if (wait_bar(smem_addr(&ms.full[tile % C::kRing][v]), (tile / C::kRing) & 1, abort_flag,
-                       &g_kv_prefill_status))
-            release(tile, v);
-        }
+        const uint32_t tile = tiles + j;
+        if (wait_bar(smem_addr(&ms.full[tile % C::kRing][0]), (tile / C::kRing) & 1, abort_flag,
+                     &g_kv_prefill_status))
+          release(tile);
       }
     }
     __syncwarp();
@@ -626,15 +575,14 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant_
     for (int i = 0; i < 2; ++i) {
       for (int s = 0; s < C::kRing; ++s) {
         mbar_init(smem_addr(&ms.full[s][i]), 1);
-        mbar_init(smem_addr(&ms.empty[s][i]), 2);
+        mbar_init(smem_addr(&ms.empty[s][i]), i == 0 ? 2 : 1);
       }
       mbar_init(smem_addr(&ms.q_full[i]), 1);
       mbar_init(smem_addr(&ms.q_empty[i]), 1);
-      mbar_init(smem_addr(&ms.o_last[i]), 1);
-      mbar_init(smem_addr(&ms.o_full[i]), 1);
       for (int b = 0; b < 2; ++b) {
         mbar_init(smem_addr(&ms.s_full[i][b]), 1);
         mbar_init(smem_addr(&ms.p_full[i][b]), 4);
+        mbar_init(smem_addr(&ms.pv_done[i][b]), 1);
       }
     }
     ms.abort_flag = 0;
@@ -645,7 +593,7 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant_
     tma_prefetch(&km);
     tma_prefetch(&vm);
   }
-  if (warp == kWarpMma) {
+  if (warp == kWarpPV) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_addr(&ms.tmem))
                  : "memory");
@@ -659,17 +607,17 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant_
 
   if (warp >= kWarpSm0) {
     softmax<T, DK, DV>(p, (warp - kWarpSm0) >> 2, sbase, tmem, ms);
-  } else if (warp < kWarpProd) {
-    if (lane == 0) mma_issuer<T, DK, DV>(p, warp - kWarpMma, sbase, tmem, ms);
   } else if (warp == kWarpProd) {
     producer<T, DK, DV>(p, &km, &vm, sbase, ms);
+  } else if (warp == kWarpPV) {
+    if (lane == 0) pv_issuer<T, DK, DV>(p, sbase, tmem, ms);
   } else {
-    q_producer<T, DK, DV>(p, &qm, sbase, ms);
+    qk_issuer<T, DK, DV>(p, warp - kWarpQK, &qm, sbase, tmem, ms);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) {
+  if (warp == kWarpPV) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
