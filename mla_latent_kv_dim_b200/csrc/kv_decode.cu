@@ -4,10 +4,12 @@
 //   lse = ln sum_t exp(s_t),          g = Hq / Hkv query heads to a key head.
 //
 // Bytes bound it: every cached value is read once for at most 2 g multiply-adds.
-// The work is a row of 64-token pages, request by request and key head by key
-// head; every SM takes an equal slice of that row, whatever the lengths, and
-// a (request, head) that a slice's border cuts leaves normalised partial
-// results that the merge kernel joins by their log-sum-exp.
+// The work is a row of units, request by request and key head by key head:
+// the 64-token pages of a (request, head) and before them kSegUnits for its
+// fixed work (queries, joining the warps).  Every SM takes an equal slice of
+// that row, whatever the lengths, and a (request, head) that a slice's border
+// cuts leaves normalised partial results that the merge kernel joins by their
+// log-sum-exp.
 //
 // A block is one TMA producer warp and eight consumer warps over a ring of
 // 64-token stages (K and V of one page of one key head, 128-byte swizzle).
@@ -38,6 +40,7 @@ constexpr int kConsumers = 8;                      // warps
 constexpr int kThreads = 32 * (kConsumers + 1);    // and the producer
 constexpr int kMaxRows = 128;                      // query heads of one row group
 constexpr int kMaxStages = 12;
+constexpr int kSegUnits = 3;  // 13 ragged requests of 16 heads: 94, 87, 71, 68, 68 us for 0 to 4
 constexpr int kSmemMax = 232448;
 constexpr int kMiscBytes = 2048;                   // barriers, stage counts, statistics
 
@@ -75,11 +78,17 @@ __device__ __forceinline__ int req_pages(const Params& p, int b) {
   return (req_len(p, b) + kPage - 1) / kPage;
 }
 
+__device__ __forceinline__ long long req_units(const Params& p, int b) {
+  const int pages = req_pages(p, b);
+  return pages ? (long long)(pages + kSegUnits) * p.Hkv * p.groups : 0;
+}
+
 // Where a slice stands in the row of units.
 struct Walk {
   int b;
   long long base;  // units before request b
-  long long pos, lo, hi;
+  long long pos, hi;
+  int emitted;     // segments so far
 };
 
 struct Segment {
@@ -87,28 +96,36 @@ struct Segment {
   int complete, slot;
 };
 
+// The slice's next segment: a slice cuts at most its first and its last, so
+// two slots a slice hold what is not complete.
 __device__ __forceinline__ bool seg_next(const Params& p, int range, Walk& w, Segment& s) {
-  if (w.pos >= w.hi) return false;
   const int tasks = p.Hkv * p.groups;
-  for (;; ++w.b) {
+  while (w.pos < w.hi) {
     const int len = req_len(p, w.b);
-    const int pages = (len + kPage - 1) / kPage;
-    const long long n = (long long)pages * tasks;
-    if (w.pos < w.base + n) {
-      const long long off = w.pos - w.base;
-      s.b = w.b;
-      s.len = len;
-      s.task = (int)(off / pages);
-      s.page0 = (int)(off - (long long)s.task * pages);
-      const long long left = w.hi - w.pos;
-      s.page1 = left < pages - s.page0 ? s.page0 + (int)left : pages;
-      s.complete = s.page0 == 0 && s.page1 == pages;
-      s.slot = 2 * range + (w.pos == w.lo ? 0 : 1);
-      w.pos += s.page1 - s.page0;
-      return true;
+    const int pages = (len + kPage - 1) / kPage, units = pages + kSegUnits;
+    const long long n = pages ? (long long)units * tasks : 0;
+    if (w.pos >= w.base + n) {
+      w.base += n;
+      ++w.b;
+      continue;
     }
-    w.base += n;
+    const long long off = w.pos - w.base;
+    s.b = w.b;
+    s.len = len;
+    s.task = (int)(off / units);
+    const int u0 = (int)(off - (long long)s.task * units);
+    const long long left = w.hi - w.pos;
+    const int u1 = left < units - u0 ? u0 + (int)left : units;
+    w.pos += u1 - u0;
+    s.page0 = max(u0 - kSegUnits, 0);
+    s.page1 = u1 - kSegUnits;
+    if (s.page1 <= s.page0) continue;  // the slice ends in the fixed work
+    s.complete = s.page0 == 0 && s.page1 == pages;
+    s.slot = 2 * range + (w.emitted ? 1 : 0);
+    ++w.emitted;
+    return true;
   }
+  return false;
 }
 
 __device__ __forceinline__ void store_out(const Params& p, int b, int h, int c, float v0, float v1) {
@@ -214,13 +231,14 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     tma_prefetch(&kmap);
     tma_prefetch(&vmap);
   }
+  // the merge may be launched beside this kernel: it waits for its end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // units before each thread's run of requests, and the request where this
   // block's slice begins
-  const int tasks = p.Hkv * p.groups;
   const int run = (p.B + kThreads - 1) / kThreads;
   const int b_lo = min(p.B, (int)threadIdx.x * run), b_hi = min(p.B, b_lo + run);
   long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += (long long)req_pages(p, b) * tasks;
+  for (int b = b_lo; b < b_hi; ++b) mine += req_units(p, b);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -239,18 +257,18 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   // `slices` blocks take one each
   const long long slices = total < p.ranges ? total : p.ranges;
   Walk w;
-  w.lo = w.hi = total;
+  w.pos = w.hi = total;
+  w.emitted = 0;
   if (range < slices) {
-    w.lo = total * range / slices;
+    w.pos = total * range / slices;
     w.hi = total * (range + 1) / slices;
   }
-  w.pos = w.lo;
-  if (w.lo >= before && w.lo < before + mine) {
+  if (w.pos >= before && w.pos < before + mine) {
     long long base = before;
     int b = b_lo;
     for (;; ++b) {
-      const long long n = (long long)req_pages(p, b) * tasks;
-      if (w.lo < base + n) break;
+      const long long n = req_units(p, b);
+      if (w.pos < base + n) break;
       base += n;
     }
     ms.b0 = b;
@@ -260,12 +278,12 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     long long base = before;
     for (int b = b_lo; b < b_hi; ++b) {
       p.base[b] = base;
-      base += (long long)req_pages(p, b) * tasks;
+      base += req_units(p, b);
     }
     if (threadIdx.x == 0) p.base[p.B] = total;
   }
   __syncthreads();
-  if (w.lo >= w.hi) return;
+  if (w.pos >= w.hi) return;
   w.b = ms.b0;
   w.base = ms.base0;
   Segment s;
@@ -314,24 +332,32 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   const int r = lane >> 2, c2 = (lane & 3) * 2;
   const int t0 = slice * C::kNT;
   bool dead = false;  // a wait gave up: no more pages, but the block's barriers are kept
-  while (seg_next(p, range, w, s)) {
+  // the queries as A fragments: rows r and r + 8 of this row block
+  uint32_t qf[DK / 16][4];
+  const int row = rb * 16 + r;
+  auto load_q = [&](const Segment& sg) {
+    const int hk = sg.task / p.groups, rg = sg.task - hk * p.groups;
+    const int nrows = min(p.g - rg * kMaxRows, kMaxRows);
+    const uint16_t* q0 = p.q + (int64_t)sg.b * p.q_sb +
+                         (int64_t)(hk * p.g + rg * kMaxRows + row) * p.q_sh + c2;
+    const uint16_t* q1 = q0 + 8 * p.q_sh;
+#pragma unroll
+    for (int k = 0; k < DK / 16; ++k) {
+      qf[k][0] = row < nrows ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k) : 0u;
+      qf[k][1] = row + 8 < nrows ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k) : 0u;
+      qf[k][2] = row < nrows ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k + 8) : 0u;
+      qf[k][3] = row + 8 < nrows ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k + 8) : 0u;
+    }
+  };
+  Segment nx;
+  bool more = seg_next(p, range, w, nx);
+  if (more) load_q(nx);
+  while (more) {
+    s = nx;
+    more = seg_next(p, range, w, nx);
     const int hk = s.task / p.groups, rg = s.task - hk * p.groups;
     const int h0 = hk * p.g + rg * kMaxRows;            // first head of the row group
     const int nrows = min(p.g - rg * kMaxRows, kMaxRows);
-    const int row = rb * 16 + r;
-    // the queries as A fragments: rows r and r + 8 of this row block
-    uint32_t qf[DK / 16][4];
-    {
-      const uint16_t* q0 = p.q + (int64_t)s.b * p.q_sb + (int64_t)(h0 + row) * p.q_sh + c2;
-      const uint16_t* q1 = q0 + 8 * p.q_sh;
-#pragma unroll
-      for (int k = 0; k < DK / 16; ++k) {
-        qf[k][0] = row < nrows ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k) : 0u;
-        qf[k][1] = row + 8 < nrows ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k) : 0u;
-        qf[k][2] = row < nrows ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k + 8) : 0u;
-        qf[k][3] = row + 8 < nrows ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k + 8) : 0u;
-      }
-    }
     float o[DV / 8][4];
 #pragma unroll
     for (int i = 0; i < DV / 8; ++i)
@@ -439,6 +465,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (lane == 0) arrive(smem_addr(&ms.empty[slot]));
     }
 
+    if (more) load_q(nx);  // on their way while the warps join
     // join the warps that share a row block
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -463,19 +490,25 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       for (int x = 0; x < C::kTS; ++x) top = fmaxf(top, ms.stat[x * RB + rb][r + 8 * j][0]);
       f[j] = m[j] == -INFINITY ? 0.f : ex2(m[j] - top);
     }
+    // all columns at once where the rows above 8 are not used, else in halves
+    const bool narrow = RB == 1 && nrows <= 8;
+    const int passes = narrow ? 1 : 2, rows_w = narrow ? 8 : 16;
+    const int cols = DV / passes;
+    for (int pass = 0; pass < passes; ++pass) {
+      if (pass) named_bar_sync(1, 32 * kConsumers);
+      float* d = join + (warp * rows_w + r) * cols + c2;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (half) named_bar_sync(1, 32 * kConsumers);
-#pragma unroll
-      for (int i = 0; i < DV / 16; ++i) {
-        float* d = join + (warp * 16 + r) * (DV / 2) + 8 * i + c2;
-        const float* x = o[half * (DV / 16) + i];
-        *reinterpret_cast<float2*>(d) = make_float2(x[0] * f[0], x[1] * f[0]);
-        *reinterpret_cast<float2*>(d + 8 * (DV / 2)) = make_float2(x[2] * f[1], x[3] * f[1]);
+      for (int i = 0; i < DV / 8; ++i) {
+        const int at = 8 * i - pass * cols;
+        if (at < 0 || at >= cols) continue;
+        *reinterpret_cast<float2*>(d + at) = make_float2(o[i][0] * f[0], o[i][1] * f[0]);
+        if (!narrow)
+          *reinterpret_cast<float2*>(d + 8 * cols + at) =
+              make_float2(o[i][2] * f[1], o[i][3] * f[1]);
       }
       named_bar_sync(1, 32 * kConsumers);
-      for (int e = threadIdx.x; e < nrows * (DV / 4); e += 32 * kConsumers) {
-        const int rw = e / (DV / 4), c = 2 * (e - rw * (DV / 4));
+      for (int e = threadIdx.x; e < nrows * (cols / 2); e += 32 * kConsumers) {
+        const int rw = e / (cols / 2), c = 2 * (e - rw * (cols / 2));
         const int blk = rw >> 4, ri = rw & 15;
         float top = -INFINITY, slr = 0.f, sle = 0.f, v0 = 0.f, v1 = 0.f;
 #pragma unroll
@@ -487,21 +520,21 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           slr += st[1] * fx;
           sle += st[2] * fx;
           const float2 v = *reinterpret_cast<const float2*>(
-              join + ((x * RB + blk) * 16 + ri) * (DV / 2) + c);
+              join + ((x * RB + blk) * rows_w + ri) * cols + c);
           v0 += v.x;
           v1 += v.y;
         }
-        const float inv = slr > 0.f ? 1.f / slr : 0.f;
+        const float inv = slr > 0.f ? 1.f / slr : (slr == 0.f ? 0.f : NAN);
         v0 *= inv;
         v1 *= inv;
-        const int col = half * (DV / 2) + c;
+        const int col = pass * cols + c;
         if (s.complete)
           store_out(p, s.b, h0 + rw, col, v0, v1);
         else
           *reinterpret_cast<float2*>(p.part_o + ((int64_t)s.slot * p.rows + rw) * DV + col) =
               make_float2(v0, v1);
-        if (half == 0 && c == 0) {
-          const float l = sle > 0.f ? (top + log2f(sle)) * kLn2 : -INFINITY;
+        if (col == 0) {
+          const float l = sle > 0.f ? (top + log2f(sle)) * kLn2 : (sle == 0.f ? -INFINITY : NAN);
           if (!s.complete)
             p.part_l[(int64_t)s.slot * p.rows + rw] = l;
           else if (p.lse)
@@ -528,9 +561,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_decode_merge_kernel(const
   const int h0 = hk * p.g + rg * kMaxRows, nrows = min(p.g - rg * kMaxRows, kMaxRows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long base = p.base[b], total = p.base[p.B];
-  const long long pages = (p.base[b + 1] - base) / tasks;
+  const long long units = (p.base[b + 1] - base) / tasks;
   constexpr int kV = DV / 32;  // values of a lane
-  if (pages == 0) {
+  if (units == 0) {
     for (int rw = warp; rw < nrows; rw += kMergeWarps) {
 #pragma unroll
       for (int i = 0; i < kV; i += 2) store_out(p, b, h0 + rw, lane * kV + i, 0.f, 0.f);
@@ -538,13 +571,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_decode_merge_kernel(const
     }
     return;
   }
-  const long long u0 = base + pages * task, u1 = u0 + pages;
+  // the task's pages are units [u0, u1)
+  const long long start = base + units * task, u0 = start + kSegUnits, u1 = start + units;
   const long long slices = total < p.ranges ? total : p.ranges;
   const int r0 = (int)(((u0 + 1) * slices - 1) / total);
   const int r1 = (int)((u1 * slices - 1) / total);
   if (r0 == r1) return;
-  // range r0 has the task as its first segment only where it begins with it
-  const int first = 2 * r0 + (total * r0 / slices >= u0 ? 0 : 1);
+  // the task is slice r0's first segment only where the slice begins with it
+  // (the unit before a task is a page of another one)
+  const int first = 2 * r0 + (total * r0 / slices >= start ? 0 : 1);
   for (int rw = warp; rw < nrows; rw += kMergeWarps) {
     float top = -INFINITY;
     for (int x = r0 + lane; x <= r1; x += 32)
@@ -649,7 +684,7 @@ Schedule schedule(const KvDecodeProblem& p, int device) {
     sms = 148;
   }
   const int64_t pages = (p.kv.cap_rows + kPage - 1) / kPage;
-  const int64_t units = pages * p.B * p.kv.Hkv * s.groups;
+  const int64_t units = (pages + kSegUnits) * p.B * p.kv.Hkv * s.groups;
   s.ranges = (int)(units < sms ? (units > 0 ? units : 1) : sms);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   s.base_bytes = up((size_t)(p.B + 1) * sizeof(long long));

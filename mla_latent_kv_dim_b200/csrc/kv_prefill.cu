@@ -632,6 +632,7 @@ __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, E
   __shared__ int top, warp_sum[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tb = 2 * p.tpt;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = threadIdx.x; i < kBuckets; i += 1024) hist[i] = 0;
   if (threadIdx.x == 0) top = 0;
   __syncthreads();
