@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 
 import torch
@@ -87,13 +86,12 @@ def lib() -> ctypes.CDLL:
                                        ctypes.c_float, ctypes.c_float, T, T, ctypes.c_void_p,
                                        ctypes.c_size_t, ctypes.c_void_p]
             L.tpla_prefill_workspace_size.argtypes = [T, _P(ctypes.c_size_t)]
-            # the kv_* entry points take descriptor addresses (see _descs)
             V, Z, I, F = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
-            L.tpla_kv_append.argtypes = [V] * 8 + [I, I, V, V, I, V]
-            L.tpla_kv_decode.argtypes = [V] * 5 + [F, V, V, V, Z, V]
-            L.tpla_kv_decode_workspace_size.argtypes = [V] * 4 + [_P(Z)]
-            L.tpla_kv_prefill.argtypes = [V] * 7 + [I, F, V, V, V, Z, V]
-            L.tpla_kv_prefill_workspace_size.argtypes = [V] * 3 + [_P(Z)]
+            L.tpla_kv_append.argtypes = [T] * 8 + [I, I, T, T, I, V]
+            L.tpla_kv_decode.argtypes = [T] * 5 + [F, T, T, V, Z, V]
+            L.tpla_kv_decode_workspace_size.argtypes = [T] * 4 + [_P(Z)]
+            L.tpla_kv_prefill.argtypes = [T] * 7 + [I, F, T, T, V, Z, V]
+            L.tpla_kv_prefill_workspace_size.argtypes = [T] * 3 + [_P(Z)]
             for f in ("tpla_kv_append", "tpla_kv_decode", "tpla_kv_decode_workspace_size",
                       "tpla_kv_prefill", "tpla_kv_prefill_workspace_size",
                       "tpla_decode_ex", "tpla_decode", "tpla_decode_workspace_size",
@@ -348,42 +346,47 @@ def prefill(q, kv_new, start, page_row, kv_cache, norm_groups=1, hadamard=False,
 
 
 # ---------------------------------------------------------------- uncompressed keys and values
-_PACKED = struct.Struct("Pii8q")  # one tpla_tensor
-_PAD = ((0, 0, 0, 0), (0, 0, 0), (0, 0), (0,), ())
+_bind = None
+_BINDING_PATH = os.path.join(_PKG, "_kvbind.so")
 
 
-def _descs(*tensors):
-    """Descriptors of the tensors in one buffer (kept by the caller for the
-    call) and their addresses (None for None): a decode step makes these
-    calls per layer, so their host time counts."""
-    size = _PACKED.size
-    buf = ctypes.create_string_buffer(size * len(tensors))
-    base = ctypes.addressof(buf)
-    at = []
-    for i, t in enumerate(tensors):
-        if t is None:
-            at.append(None)
-            continue
-        if t.dtype not in _DT:
-            raise TypeError(f"unsupported dtype {t.dtype}")
-        n = t.dim()
-        if n > 4:
-            raise ValueError("at most 4 dimensions")
-        pad = _PAD[n]
-        _PACKED.pack_into(buf, i * size, t.data_ptr(), _DT[t.dtype], n, *t.shape, *pad,
-                          *t.stride(), *pad)
-        at.append(base + i * size)
-    return buf, at
+def _binding():
+    """The extension that marshals the kv_* calls (csrc/kv_binding.cpp), built
+    in-tree like the library; it calls the library loaded by ``lib``."""
+    global _bind
+    if _bind is not None:
+        return _bind
+    L = lib()
+    with _lock:
+        if _bind is None:
+            if not os.path.exists(_BINDING_PATH):
+                from . import build as _build
+                _build.build()
+            from . import _kvbind
+            _kvbind.init(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+                "tpla_kv_append", "tpla_kv_decode_workspace_size", "tpla_kv_decode",
+                "tpla_kv_prefill_workspace_size", "tpla_kv_prefill")))
+            _bind = _kvbind
+    return _bind
 
 
-def _scratch(workspace, need, device):
-    """A workspace of at least ``need`` bytes (the caller's where it is large
-    enough): (the tensor to keep, address, bytes)."""
-    if not need:
-        return None, None, 0
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+def _kv_check(fn: str, rc: int, tensors, workspace=None) -> None:
+    """Raises for a status of the binding: a wrong device or a tensor without
+    a descriptor as everywhere in this module, else the library's status."""
+    if rc > 0:
+        _on_current_device(*tensors, workspace)
+        for t in tensors:
+            desc(t)
+        raise RuntimeError(f"{fn}: binding status {rc}")
+    _check(fn, rc)
+
+
+def _stream_context(stream):
+    """Context in which ``stream`` (a torch stream or a raw handle) is the
+    current one, so that what a call allocates belongs to it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def kv_append(k_new, v_new, positions, page_table, k_cache, v_cache, *, requests=None,
@@ -397,18 +400,20 @@ def kv_append(k_new, v_new, positions, page_table, k_cache, v_cache, *, requests
     None (a cache of one tensor, such as latent rows with their rope columns).
     In place on the caches; returns the rotated queries (``q_out``, which may
     be ``q``), or None without ``q``."""
-    _on_current_device(k_new, v_new, positions, page_table, k_cache, v_cache, requests, cos_sin,
-                       q, q_out)
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=k_cache.dtype, device=q.device)
-    if q_rope_offset is None:
-        q_rope_offset = rope_offset
-    buf, d = _descs(k_new, v_new, positions, requests, page_table, k_cache, v_cache, cos_sin, q,
-                    q_out)
-    rc = lib().tpla_kv_append(*d[:8], int(rope_offset), 1 if interleaved else 0, d[8], d[9],
-                              int(q_rope_offset), _stream(stream))
-    _check("tpla_kv_append", rc)
-    return q_out
+    if stream is not None:
+        with _stream_context(stream):
+            return kv_append(k_new, v_new, positions, page_table, k_cache, v_cache,
+                             requests=requests, cos_sin=cos_sin, rope_offset=rope_offset,
+                             interleaved=interleaved, q=q, q_out=q_out,
+                             q_rope_offset=q_rope_offset)
+    rc, result = (_bind or _binding()).kv_append(
+        k_new, v_new, positions, requests, page_table, k_cache, v_cache, cos_sin, q, q_out,
+        rope_offset, 1 if interleaved else 0,
+        rope_offset if q_rope_offset is None else q_rope_offset)
+    if rc:
+        _kv_check("tpla_kv_append", rc, (k_new, v_new, positions, requests, page_table, k_cache,
+                                         v_cache, cos_sin, q, q_out))
+    return result if q_out is None else q_out
 
 
 def kv_decode(q, k_cache, v_cache, seq_lens, page_table, scale=None, out=None, lse=None, *,
@@ -419,20 +424,17 @@ def kv_decode(q, k_cache, v_cache, seq_lens, page_table, scale=None, out=None, l
     (tpla_kv_decode).  Returns (out [B, Hq, Dv], lse [B, Hq, 1])."""
     if scale is None:
         raise ValueError("scale is required")
-    _on_current_device(q, k_cache, v_cache, seq_lens, page_table, out, lse, workspace)
-    if out is None:
-        out = torch.empty((q.shape[0], q.shape[1], v_cache.shape[-1]), dtype=out_dtype,
-                          device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty((q.shape[0], q.shape[1], 1), dtype=torch.float32, device=q.device)
-    buf, d = _descs(q, k_cache, v_cache, seq_lens, page_table, out, lse)
-    n = ctypes.c_size_t(0)
-    _check("tpla_kv_decode_workspace_size",
-           lib().tpla_kv_decode_workspace_size(d[0], d[1], d[2], d[4], ctypes.byref(n)))
-    workspace, ws, size = _scratch(workspace, n.value, q.device)
-    rc = lib().tpla_kv_decode(*d[:5], scale, d[5], d[6], ws, size, _stream(stream))
-    _check("tpla_kv_decode", rc)
-    return out, lse
+    if stream is not None:
+        with _stream_context(stream):
+            return kv_decode(q, k_cache, v_cache, seq_lens, page_table, scale, out, lse,
+                             workspace=workspace, out_dtype=out_dtype, want_lse=want_lse)
+    rc, out_, lse_ = (_bind or _binding()).kv_decode(
+        q, k_cache, v_cache, seq_lens, page_table, out, lse, workspace, scale, _DT[out_dtype],
+        1 if want_lse else 0)
+    if rc:
+        _kv_check("tpla_kv_decode", rc, (q, k_cache, v_cache, seq_lens, page_table, out, lse),
+                  workspace)
+    return out_ if out is None else out, lse_ if lse is None else lse
 
 
 def kv_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, seq_lens=None, page_table=None,
@@ -447,21 +449,18 @@ def kv_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, seq_lens=None, page_
     token up with the last key.  Returns (out [T, Hq, Dv], lse [T, Hq, 1])."""
     if scale is None:
         raise ValueError("scale is required")
-    _on_current_device(q, k, v, cu_seqlens_q, cu_seqlens_k, seq_lens, page_table, out, lse,
-                       workspace)
-    if out is None:
-        out = torch.empty((q.shape[0], q.shape[1], v.shape[-1]), dtype=out_dtype, device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty((q.shape[0], q.shape[1], 1), dtype=torch.float32, device=q.device)
-    buf, d = _descs(q, k, v, cu_seqlens_q, cu_seqlens_k, seq_lens, page_table, out, lse)
-    n = ctypes.c_size_t(0)
-    _check("tpla_kv_prefill_workspace_size",
-           lib().tpla_kv_prefill_workspace_size(d[0], d[1], d[3], ctypes.byref(n)))
-    workspace, ws, size = _scratch(workspace, n.value, q.device)
-    rc = lib().tpla_kv_prefill(*d[:7], 1 if causal else 0, scale, d[7], d[8], ws, size,
-                               _stream(stream))
-    _check("tpla_kv_prefill", rc)
-    return out, lse
+    if stream is not None:
+        with _stream_context(stream):
+            return kv_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, seq_lens=seq_lens,
+                              page_table=page_table, scale=scale, causal=causal, out=out, lse=lse,
+                              workspace=workspace, out_dtype=out_dtype, want_lse=want_lse)
+    rc, out_, lse_ = (_bind or _binding()).kv_prefill(
+        q, k, v, cu_seqlens_q, cu_seqlens_k, seq_lens, page_table, out, lse, workspace,
+        1 if causal else 0, scale, _DT[out_dtype], 1 if want_lse else 0)
+    if rc:
+        _kv_check("tpla_kv_prefill", rc, (q, k, v, cu_seqlens_q, cu_seqlens_k, seq_lens,
+                                          page_table, out, lse), workspace)
+    return out_ if out is None else out, lse_ if lse is None else lse
 
 
 def device_status(stream=None) -> int:

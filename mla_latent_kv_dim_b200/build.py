@@ -1,4 +1,5 @@
-"""Build libtpla.so in-tree with nvcc for sm_100a.
+"""Build libtpla.so in-tree with nvcc for sm_100a, and the Python extension
+_kvbind.so beside it.
 
 Usage: python -m mla_latent_kv_dim_b200.build [--force]
 """
@@ -15,6 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtpla.so")
+BINDING = os.path.join(PKG, "_kvbind.so")
 SOURCES = ["api.cu", "decode_generic.cu", "decode_sm100.cu", "merge.cu", "hadamard.cu",
            "vup.cu", "noalloc.cu", "pca.cu", "append.cu", "kv_api.cu", "kv_append.cu", "kv_decode.cu",
            "kv_prefill.cu"]
@@ -41,6 +43,24 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_command() -> list[str]:
+    """g++ command of the Python extension that marshals the tpla_kv_* calls
+    (torch's headers and libraries; no CUDA code)."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"],
+            "-isystem", os.path.join(base, "include"),
+            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"),
+            os.path.join(CSRC, "kv_binding.cpp"), "-o", BINDING,
+            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     nvcc = _nvcc()
@@ -54,17 +74,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(o)
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, *_flags(), "-c", s, "-o", o])
+    compiled = bool(jobs)
+    if force or _stale(BINDING, [os.path.join(CSRC, "kv_binding.cpp"), headers[0]]):
+        jobs.append(_binding_command())
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+            raise RuntimeError("compiler failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr)
 
     with ThreadPoolExecutor(max_workers=min(8, max(1, len(jobs)))) as ex:
         list(ex.map(run, jobs))
-    if force or jobs or _stale(LIB, objs):
+    if force or compiled or _stale(LIB, objs):
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", LIB, *objs,
              "-Xlinker", "--no-undefined", "-ldl"])
     return LIB
