@@ -490,7 +490,8 @@ TPLA_API int tpla_kv_decode(const tpla_tensor* q, const tpla_tensor* k_cache,
  * Limits (TPLA_ERR_UNSUPPORTED): B <= 2^20, T and Tk <= 2^30, Hq <= 4096.
  */
 TPLA_API int tpla_kv_prefill_workspace_size(const tpla_tensor* q, const tpla_tensor* k,
-                                            const tpla_tensor* cu_q, size_t* bytes);
+                                            const tpla_tensor* v, const tpla_tensor* cu_q,
+                                            const tpla_tensor* page_table, size_t* bytes);
 TPLA_API int tpla_kv_prefill(const tpla_tensor* q, const tpla_tensor* k, const tpla_tensor* v,
                              const tpla_tensor* cu_q, const tpla_tensor* cu_k,
                              const tpla_tensor* seq_lens, const tpla_tensor* page_table,

@@ -91,7 +91,7 @@ def lib() -> ctypes.CDLL:
             L.tpla_kv_decode.argtypes = [T] * 5 + [F, T, T, V, Z, V]
             L.tpla_kv_decode_workspace_size.argtypes = [T] * 4 + [_P(Z)]
             L.tpla_kv_prefill.argtypes = [T] * 7 + [I, F, T, T, V, Z, V]
-            L.tpla_kv_prefill_workspace_size.argtypes = [T] * 3 + [_P(Z)]
+            L.tpla_kv_prefill_workspace_size.argtypes = [T] * 5 + [_P(Z)]
             for f in ("tpla_kv_append", "tpla_kv_decode", "tpla_kv_decode_workspace_size",
                       "tpla_kv_prefill", "tpla_kv_prefill_workspace_size",
                       "tpla_decode_ex", "tpla_decode", "tpla_decode_workspace_size",

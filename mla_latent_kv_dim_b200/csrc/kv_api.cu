@@ -412,18 +412,24 @@ int tpla_kv_decode(const tpla_tensor* q, const tpla_tensor* k_cache, const tpla_
 }
 
 int tpla_kv_prefill_workspace_size(const tpla_tensor* q, const tpla_tensor* k,
-                                   const tpla_tensor* cu_q, size_t* bytes) {
-  if (!bytes || !q || !k || !cu_q || q->ndim != 3 || cu_q->ndim != 1 || cu_q->shape[0] < 1 ||
-      (k->ndim != 3 && k->ndim != 4))
+                                   const tpla_tensor* v, const tpla_tensor* cu_q,
+                                   const tpla_tensor* page_table, size_t* bytes) {
+  if (!bytes || !q || !k || !v || !cu_q || q->ndim != 3 || cu_q->ndim != 1 ||
+      cu_q->shape[0] < 1 || k->ndim != (page_table ? 4 : 3) || v->ndim != k->ndim ||
+      (page_table && page_table->ndim != 2))
     return TPLA_ERR_INVALID_ARG;
-  const int64_t Hkv = k->shape[k->ndim - 2];
-  if (q->shape[0] < 0 || Hkv < 1 || q->shape[1] < 1 || q->shape[1] % Hkv)
+  const int64_t Hkv = k->shape[k->ndim - 2], Dv = v->shape[v->ndim - 1];
+  const int64_t cap = page_table ? page_table->shape[1] * kBlock : k->shape[0];
+  if (q->shape[0] < 0 || Hkv < 1 || q->shape[1] < 1 || q->shape[1] % Hkv || Dv < 1 || cap < 0)
     return TPLA_ERR_INVALID_ARG;
-  if (q->shape[0] > kMaxRows || q->shape[1] > kMaxHeads || cu_q->shape[0] - 1 > kMaxBatch)
+  if (q->shape[0] > kMaxRows || q->shape[1] > kMaxHeads || cu_q->shape[0] - 1 > kMaxBatch ||
+      cap > kMaxRows || Dv > 4096)
     return TPLA_ERR_UNSUPPORTED;
   KvPrefillProblem p;
   memset(&p, 0, sizeof(p));
   p.kv.Hkv = (int)Hkv;
+  p.kv.Dv = (int)Dv;
+  p.kv.cap_rows = cap;
   p.T = (int)q->shape[0];
   p.Hq = (int)q->shape[1];
   p.B = (int)cu_q->shape[0] - 1;

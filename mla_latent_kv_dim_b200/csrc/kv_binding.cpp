@@ -231,7 +231,7 @@ PyObject* py_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (t[8].none && want) make(&t[8], {q.size(0), q.size(1), 1}, q, at::kFloat);
     }
     size_t need = 0, bytes = 0;
-    rc = g_prefill_ws(t[0].ptr(), t[1].ptr(), t[3].ptr(), &need);
+    rc = g_prefill_ws(t[0].ptr(), t[1].ptr(), t[2].ptr(), t[3].ptr(), t[6].ptr(), &need);
     if (rc == TPLA_OK) {
       void* w = workspace(&ws, need, t[0].t, &bytes);
       rc = g_prefill(t[0].ptr(), t[1].ptr(), t[2].ptr(), t[3].ptr(), t[4].ptr(), t[5].ptr(),

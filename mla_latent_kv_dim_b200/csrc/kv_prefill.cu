@@ -27,7 +27,10 @@
 //  * K and V tiles go through a ring of key tiles (64-column chunks of 64 rows,
 //    128-byte swizzle, K-major for Q K^T and MN-major for P V);
 //  * items are handed out longest first (a small kernel sorts them; one
-//    request needs no sorting), so the last ones are short.
+//    request needs no sorting), so the last ones are short.  Where a call has
+//    too few items for the GPU (a short chunk after a long prefix), that
+//    kernel cuts their keys into pieces, whose normalised results a third
+//    kernel joins by their log-sum-exp.
 #include <cuda_runtime.h>
 
 #include <mutex>
@@ -59,12 +62,21 @@ constexpr int kBuckets = 2048;  // of the items' lengths
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
+constexpr int kMinPiece = 8;  // key tiles; a shorter piece is mostly fixed work
+
 struct Entry {  // two query tiles of one request
   int t0;       // first token within the request
   int q0, qlen; // the request's rows of q
   int k0;       // packed: its first row of k
   int kvlen;    // its keys
-  int b, pad0, pad1;
+  int b;
+  int j0, j1;   // key tiles of this piece
+  int slot;     // of its partial result (times the heads), -1: the whole item
+  int pad[3];
+};
+
+struct Join {  // an item in pieces
+  int t0, q0, qlen, slot, pieces, pad[3];
 };
 
 struct Params {
@@ -76,10 +88,15 @@ struct Params {
   int causal;
   float scale_log2;      // |softmax scale| * log2(e) (> 0; see the launcher)
   int negate;            // scale < 0
-  const int* count;      // entries of the list, or null: one request, no list
+  const int* count;      // entries of the list (and of joins), or null: one request, no list
   const Entry* list;
+  const Join* joins;
+  float* part_o;         // [slot * heads + head, Dv / 4, rows_slot, 4]
+  float* part_l;         // [slot * heads + head, rows_slot]
+  int rows_slot;         // 2 tpt gg, less where the call has fewer tokens
   void* out;
   int out_dtype;
+  int out32;             // 16-bit rows on 32-byte boundaries
   int64_t o_st, o_sh;
   float* lse;
   int64_t l_st, l_sh;
@@ -88,7 +105,8 @@ struct Params {
 struct Item {
   Entry e;
   int hk, rg;
-  int n[2];  // key tiles of the two query tiles
+  int slot;
+  int n[2];  // key tiles of the two query tiles in this piece
   int nmax;
 };
 
@@ -167,14 +185,20 @@ struct Items {
       int4* d = reinterpret_cast<int4*>(&it.e);
       d[0] = s[0];
       d[1] = s[1];
+      d[2] = s[2];
     } else {  // longest first: the last tokens of a causal prompt see the most keys
       request(p, 0, it.e);
       it.e.t0 = (total / heads - 1 - x) * 2 * p.tpt;
+      it.e.j0 = 0;
+      it.e.j1 = 1 << 30;
+      it.e.slot = -1;
     }
+    it.slot = it.e.slot < 0 ? -1 : it.e.slot * heads + h;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int a = it.e.t0 + t * p.tpt, z = min(a + p.tpt, it.e.qlen);
-      it.n[t] = z > a ? (limit_of(p, it.e, z - 1) + kKeys - 1) / kKeys : 0;
+      const int n = z > a ? (limit_of(p, it.e, z - 1) + kKeys - 1) / kKeys : 0;
+      it.n[t] = max(0, min(n, it.e.j1) - it.e.j0);
     }
     it.nmax = max(it.n[0], it.n[1]);
     // A query tile that sees no key, or has no rows, takes part with all its
@@ -230,10 +254,12 @@ __device__ void producer(const Params& p, const CUtensorMap* km, const CUtensorM
   while (items.next(p, it)) {
     int win = 0;  // lane i: the page id of key tile 32 w + i
     for (int j = 0; j < it.nmax; ++j, ++tile) {
-      int page = 0, row = it.e.k0 + kKeys * j, flag = 0;
+      int page = 0, row = it.e.k0 + kKeys * (it.e.j0 + j), flag = 0;
       if (p.page_table) {
         if ((j & 31) == 0)
-          win = j + lane < it.nmax ? p.page_table[(int64_t)it.e.b * p.pt_sb + j + lane] : 0;
+          win = j + lane < it.nmax
+                    ? p.page_table[(int64_t)it.e.b * p.pt_sb + it.e.j0 + j + lane]
+                    : 0;
         page = __shfl_sync(0xffffffffu, win, j & 31);
         row = 0;
         if (page < 0 || page >= p.num_blocks) {
@@ -406,7 +432,8 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
     const int head = it.rg * p.gg + my_head;
     const bool live = my_tok < p.tpt && tok < it.e.qlen && head < p.g;
     // rows past the tile's tokens or the request's are computed and not stored
-    const int limit = live ? limit_of(p, it.e, tok) : it.e.kvlen;
+    const int held = it.e.kvlen - kKeys * it.e.j0;  // keys from this piece's first on
+    const int limit = (live ? limit_of(p, it.e, tok) : it.e.kvlen) - kKeys * it.e.j0;
     const int n = t ? it.n[1] : it.n[0];
     float m = -INFINITY, l = 0.f, lx = 0.f;  // maximum; sums of the 16-bit and the f32 weights
     for (int j = 0; j < n; ++j, ++cnt) {
@@ -464,7 +491,7 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
         }
         tmem_wait_st();
       }
-      const int left = it.e.kvlen - kKeys * j;
+      const int left = held - kKeys * j;
       if (left < kKeys) {
         // behind the request's last key stand other rows or stale ones; a
         // weight of 0 does not stop an infinity or a NaN there, so they are
@@ -520,7 +547,15 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
     __syncwarp();
     tiles += it.nmax;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : NAN);
+    // the row's place: in the output, or (f32) in the piece's slot
     const int64_t orow = (int64_t)(it.e.q0 + tok) * p.o_st + (int64_t)(it.hk * p.g + head) * p.o_sh;
+    const int64_t prow =
+        (int64_t)it.slot * p.rows_slot + (t * p.tpt + my_tok) * p.gg + my_head;
+    const int prows = p.rows_slot;
+    float* const part = p.part_o + ((int64_t)it.slot * (DV / 4) * prows + (t * p.tpt + my_tok) * p.gg +
+                                    my_head) * 4;
+    float* const frow = reinterpret_cast<float*>(p.out) + orow;
+    uint16_t* const hrow = reinterpret_cast<uint16_t*>(p.out) + orow;
 #pragma unroll
     for (int c = 0; c < DV; c += 32) {
       uint32_t o[32];
@@ -532,30 +567,42 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
         for (int k = 0; k < 32; ++k) o[k] = 0u;
       }
       if (live) {
-        if (p.out_dtype == TPLA_F32) {
-          float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + orow + c);
+        if (it.slot >= 0) {  // the rows of a warp lie side by side
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            d[k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
-                               __uint_as_float(o[4 * k + 2]) * inv,
-                               __uint_as_float(o[4 * k + 3]) * inv);
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(part + (int64_t)((c + k) / 4) * prows * 4) = make_float4(
+                __uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv,
+                __uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv);
+        } else if (p.out_dtype == TPLA_F32) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(frow + c + k) = make_float4(
+                __uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv,
+                __uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv);
         } else {
-          uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + orow + c);
+          uint32_t v[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t v[4];
+          for (int k = 0; k < 16; ++k)
+            v[k] = T::pack(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+          if (p.out32) {  // a thread's stores lie in lines of their own: the fewer the better
+            st_global_v8(hrow + c, v);
+            st_global_v8(hrow + c + 16, v + 8);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              v[i] = T::pack(__uint_as_float(o[8 * k + 2 * i]) * inv,
-                             __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
-            d[k] = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<uint4*>(hrow + c + 2 * k) =
+                  make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
           }
         }
       }
     }
-    if (live && p.lse)
-      p.lse[(int64_t)(it.e.q0 + tok) * p.l_st + (int64_t)(it.hk * p.g + head) * p.l_sh] =
-          lx > 0.f ? (m + log2f(lx)) * kLn2 : (lx == 0.f ? -INFINITY : NAN);
+    if (live && (p.lse || it.slot >= 0)) {
+      const float lse = lx > 0.f ? (m + log2f(lx)) * kLn2 : (lx == 0.f ? -INFINITY : NAN);
+      if (it.slot >= 0)
+        p.part_l[prow] = lse;
+      else
+        p.lse[(int64_t)(it.e.q0 + tok) * p.l_st + (int64_t)(it.hk * p.g + head) * p.l_sh] = lse;
+    }
     tc_fence_before();
   }
 }
@@ -626,16 +673,28 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant_
 // The list of items, longest first: a counting sort by the key tiles of each
 // item's last token.  One block; a warp takes a request at a time.  The order
 // within a bucket is not fixed, and no result depends on it.
+//
+// With `slots` > 0 items may be cut: the work of a call with few items is
+// meant to fill `fill` blocks twice, so no piece is longer than that share.
 __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, Entry* list,
-                                                               int* count, int capacity) {
+                                                               Join* joins, int* count,
+                                                               int capacity, int slots,
+                                                               int fill) {
   __shared__ int hist[kBuckets];
-  __shared__ int top, warp_sum[32];
+  __shared__ int top, warp_sum[32], n_joins, n_slots;
+  __shared__ unsigned long long work;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tb = 2 * p.tpt;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = threadIdx.x; i < kBuckets; i += 1024) hist[i] = 0;
-  if (threadIdx.x == 0) top = 0;
+  if (threadIdx.x == 0) {
+    top = n_joins = n_slots = 0;
+    work = 0;
+  }
   __syncthreads();
+  auto tiles_of = [&](const Entry& e, int t0) {
+    return (limit_of(p, e, min(t0 + tb, e.qlen) - 1) + kKeys - 1) / kKeys;
+  };
   int most = 0;
   for (int b = threadIdx.x; b < p.B; b += 1024) {
     Entry e;
@@ -643,17 +702,31 @@ __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, E
     most = max(most, (e.kvlen + kKeys - 1) / kKeys);
   }
   if (most) atomicMax(&top, most);
+  if (slots > 0) {
+    unsigned long long mine = 0;
+    for (int b = warp; b < p.B; b += 32) {
+      Entry e;
+      request(p, b, e);
+      for (int t0 = lane * tb; t0 < e.qlen; t0 += 32 * tb) mine += tiles_of(e, t0);
+    }
+    if (mine) atomicAdd(&work, mine);
+  }
   __syncthreads();
   int shift = 0;
   while ((top >> shift) >= kBuckets) ++shift;
-  auto bucket = [&](const Entry& e, int t0) {  // 0 for the longest
-    const int tiles = (limit_of(p, e, min(t0 + tb, e.qlen) - 1) + kKeys - 1) / kKeys;
-    return kBuckets - 1 - (tiles >> shift);
-  };
+  const int heads = p.Hkv * p.groups;
+  const int share = (int)min((unsigned long long)(1 << 30),
+                             (work * heads + 2 * fill - 1) / (unsigned long long)(2 * fill));
+  const int longest = max(kMinPiece, share);
+  auto pieces_of = [&](int tiles) { return slots > 0 ? max(1, (tiles + longest - 1) / longest) : 1; };
+  auto bucket = [&](int tiles) { return kBuckets - 1 - (tiles >> shift); };  // 0: the longest
   for (int b = warp; b < p.B; b += 32) {
     Entry e;
     request(p, b, e);
-    for (int t0 = lane * tb; t0 < e.qlen; t0 += 32 * tb) atomicAdd(&hist[bucket(e, t0)], 1);
+    for (int t0 = lane * tb; t0 < e.qlen; t0 += 32 * tb) {
+      const int tiles = tiles_of(e, t0), k = pieces_of(tiles);
+      atomicAdd(&hist[bucket((tiles + k - 1) / k)], k);
+    }
   }
   __syncthreads();
   {  // exclusive prefix of the buckets, two to a thread
@@ -670,24 +743,113 @@ __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, E
     for (int i = 0; i < warp; ++i) before += warp_sum[i];
     hist[2 * threadIdx.x] = before;
     hist[2 * threadIdx.x + 1] = before + a;
-    if (threadIdx.x == 1023) *count = min(before + a + z, capacity);
+    if (threadIdx.x == 1023) count[0] = min(before + a + z, capacity);
   }
   __syncthreads();
   for (int b = warp; b < p.B; b += 32) {
     Entry e;
     request(p, b, e);
-    e.pad0 = e.pad1 = 0;
+    e.pad[0] = e.pad[1] = e.pad[2] = 0;
     for (int t0 = lane * tb; t0 < e.qlen; t0 += 32 * tb) {
-      const int at = atomicAdd(&hist[bucket(e, t0)], 1);
-      if (at < capacity) {  // requests that overlap in q can ask for more
-        e.t0 = t0;
-        const int4* s = reinterpret_cast<const int4*>(&e);
-        int4* d = reinterpret_cast<int4*>(list + at);
+      const int tiles = tiles_of(e, t0), k = pieces_of(tiles), len = (tiles + k - 1) / k;
+      e.t0 = t0;
+      e.slot = -1;
+      const int at = atomicAdd(&hist[bucket(len)], k);
+      if (at + k > capacity) {  // requests that overlap in q can ask for more
+        bounds();
+        for (int i = at; i < capacity; ++i) list[i].qlen = list[i].kvlen = list[i].t0 = 0;
+        continue;
+      }
+      if (k > 1) {
+        const int slot = atomicAdd(&n_slots, k);
+        if (slot + k <= slots) {
+          const int j = atomicAdd(&n_joins, 1);
+          joins[j] = Join{t0, e.q0, e.qlen, slot, k, {0, 0, 0}};
+          e.slot = slot;
+        }
+      }
+      for (int i = 0; i < k; ++i) {
+        // without a slot (see above) the first piece is the whole item and
+        // the others are empty
+        const bool whole = e.slot < 0;
+        Entry x = e;
+        x.j0 = whole ? 0 : i * len;
+        x.j1 = whole ? 1 << 30 : min(tiles, (i + 1) * len);
+        x.slot = whole ? -1 : e.slot + i;
+        if (whole && i > 0) x.qlen = x.t0 = x.kvlen = 0;
+        const int4* s = reinterpret_cast<const int4*>(&x);
+        int4* d = reinterpret_cast<int4*>(list + at + i);
         d[0] = s[0];
         d[1] = s[1];
-      } else {
-        bounds();
+        d[2] = s[2];
       }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) count[1] = n_joins;
+}
+
+// Joins the pieces of an item,
+//   lse = ln sum_i exp(lse_i),  out = sum_i exp(lse_i - lse) out_i:
+// a thread per row and 8 columns, the rows of a warp side by side.
+constexpr int kJoinThreads = 128;
+
+template <int DV>
+__global__ void __launch_bounds__(kJoinThreads) kv_prefill_join_kernel(const Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int heads = p.Hkv * p.groups, n = p.count[1];
+  constexpr int kC = DV / 8;  // column groups of a row
+  const int rows = p.rows_slot;
+  for (int x = blockIdx.x; x < n * heads; x += gridDim.x) {
+    const Join jn = p.joins[x / heads];
+    const int h = x % heads, hk = h / p.groups, rg = h - hk * p.groups;
+    for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < rows * kC;
+         e += gridDim.y * kJoinThreads) {
+      const int c = e / rows, row = e - c * rows;
+      const int tok = jn.t0 + row / p.gg, head = rg * p.gg + row % p.gg;
+      if (tok >= jn.qlen || head >= p.g) continue;
+      const float* l = p.part_l + ((int64_t)jn.slot * heads + h) * rows + row;
+      const float4* o = reinterpret_cast<const float4*>(p.part_o) +
+                        (((int64_t)jn.slot * heads + h) * (DV / 4) + 2 * c) * rows + row;
+      const int64_t step = (int64_t)heads * rows;  // between two pieces
+      float top = -INFINITY;
+      for (int i = 0; i < jn.pieces; ++i) top = fmaxf(top, l[i * step]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < jn.pieces; ++i) {
+        const float w = expf(l[i * step] - ref);
+        const float4 a = o[i * step * (DV / 4)], b = o[i * step * (DV / 4) + rows];
+        sum += w;
+        acc[0] = fmaf(w, a.x, acc[0]);
+        acc[1] = fmaf(w, a.y, acc[1]);
+        acc[2] = fmaf(w, a.z, acc[2]);
+        acc[3] = fmaf(w, a.w, acc[3]);
+        acc[4] = fmaf(w, b.x, acc[4]);
+        acc[5] = fmaf(w, b.y, acc[5]);
+        acc[6] = fmaf(w, b.z, acc[6]);
+        acc[7] = fmaf(w, b.w, acc[7]);
+      }
+      const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : NAN);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] *= inv;
+      const int64_t off = (int64_t)(jn.q0 + tok) * p.o_st + (int64_t)(hk * p.g + head) * p.o_sh +
+                          8 * c;
+      if (p.out_dtype == TPLA_F32) {
+        float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + off);
+        d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        d[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      } else {
+        uint32_t v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = p.out_dtype == TPLA_F16 ? F16::pack(acc[2 * k], acc[2 * k + 1])
+                                         : Bf16::pack(acc[2 * k], acc[2 * k + 1]);
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + off) =
+            make_uint4(v[0], v[1], v[2], v[3]);
+      }
+      if (p.lse && c == 0)
+        p.lse[(int64_t)(jn.q0 + tok) * p.l_st + (int64_t)(hk * p.g + head) * p.l_sh] =
+            sum > 0.f ? ref + logf(sum) : (sum == 0.f ? -INFINITY : NAN);
     }
   }
 }
@@ -695,18 +857,51 @@ __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, E
 // ---------------------------------------------------------------- host side
 
 struct Shape {
-  int g, gg, groups, tpt;
+  int g, gg, groups, tpt, heads, sms;
   int64_t entries;  // most items of a head: ceil(T_b / (2 tpt)) summed over the requests
+  bool planned;     // the list of items is made by the plan kernel
+  int slots;        // partial results (times the heads) of items in pieces, 0: none are cut
+  int rows_slot;
+  int64_t capacity; // entries of the list
+  size_t list_bytes, join_bytes, o_bytes, l_bytes;
 };
 
-Shape shape(const KvPrefillProblem& p) {
+Shape shape(const KvPrefillProblem& p, int sms) {
   Shape s;
   s.g = p.Hq / p.kv.Hkv;
   s.gg = s.g < kRows ? s.g : kRows;
   s.groups = (s.g + s.gg - 1) / s.gg;
   s.tpt = kRows / s.gg;
+  s.heads = p.kv.Hkv * s.groups;
+  s.sms = sms;
   s.entries = (int64_t)p.T / (2 * s.tpt) + p.B;
+  // Items are cut where full ones would not go round the GPU twice and the
+  // keys are long enough for two pieces.  Cutting makes no piece longer than
+  // half a block's share of the work: at most 2 sms pieces of that length,
+  // and twice as many in all.
+  const bool cut = (int64_t)p.T / (2 * s.tpt) * s.heads < 2 * sms &&
+                   p.kv.cap_rows >= 2 * kMinPiece * kKeys;
+  s.planned = p.B > 1 || cut;
+  s.slots = cut ? (4 * sms + s.heads - 1) / s.heads : 0;
+  s.rows_slot = (p.T < 2 * s.tpt ? p.T : 2 * s.tpt) * s.gg;
+  s.capacity = s.entries + (cut ? 2 * sms : 0);
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  s.list_bytes = up((size_t)s.capacity * sizeof(Entry));
+  s.join_bytes = up((size_t)s.slots * sizeof(Join));
+  const size_t rows = (size_t)s.slots * s.heads * s.rows_slot;
+  s.o_bytes = up(rows * p.kv.Dv * sizeof(float));
+  s.l_bytes = up(rows * sizeof(float));
   return s;
+}
+
+int sm_count(int device) {
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+      sms < 1) {
+    cudaGetLastError();
+    sms = 148;
+  }
+  return sms;
 }
 
 template <typename T, int DK, int DV>
@@ -736,6 +931,12 @@ cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorM
   cfg.numAttrs = p.count ? 1 : 0;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_prefill_kernel<T, DK, DV>, qm, km, vm, p);
   count_launch();
+  if (e != cudaSuccess || !p.part_o) return e;
+  cfg.gridDim = dim3(64, 8);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, kv_prefill_join_kernel<DV>, p);
+  count_launch();
   return e;
 }
 
@@ -751,18 +952,15 @@ cudaError_t launch_type(const CUtensorMap& qm, const CUtensorMap& km, const CUte
 }  // namespace
 
 size_t kv_prefill_workspace_bytes(const KvPrefillProblem& p) {
-  if (p.B <= 1) return 0;
-  return 256 + (size_t)shape(p).entries * sizeof(Entry);
+  const Shape s = shape(p, sm_count(current_device()));
+  return s.planned ? 256 + s.list_bytes + s.join_bytes + s.o_bytes + s.l_bytes : 0;
 }
 
 cudaError_t launch_kv_prefill(const KvPrefillProblem& dp, void* ws, cudaStream_t stream) {
   const int dev = current_device();
   if (!sm100_device(dev)) return cudaErrorNotSupported;
-  int sms = 0;
-  cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   const KvSource& kv = dp.kv;
-  const Shape s = shape(dp);
+  const Shape s = shape(dp, sm_count(dev));
   CUtensorMap qm, km, vm;
   {
     const cuuint64_t dims[5] = {64, (cuuint64_t)s.g, (cuuint64_t)dp.T, (cuuint64_t)(kv.Dk / 64),
@@ -806,19 +1004,31 @@ cudaError_t launch_kv_prefill(const KvPrefillProblem& dp, void* ws, cudaStream_t
   p.lse = dp.lse;
   p.l_st = dp.l_st;
   p.l_sh = dp.l_sh;
-  const int64_t items = s.entries * kv.Hkv * s.groups;
-  if (items > (1LL << 31) - 1 - sms) return cudaErrorInvalidValue;
-  if (dp.B > 1) {
-    int* count = reinterpret_cast<int*>(ws);
-    Entry* list = reinterpret_cast<Entry*>(reinterpret_cast<char*>(ws) + 256);
-    kv_prefill_plan_kernel<<<1, 1024, 0, stream>>>(p, list, count, (int)s.entries);
+  p.out32 = dp.out_dtype != TPLA_F32 && (reinterpret_cast<uintptr_t>(dp.out) & 31) == 0 &&
+            (dp.T == 1 || dp.o_st % 16 == 0) && (dp.Hq == 1 || dp.o_sh % 16 == 0);
+  p.rows_slot = s.rows_slot;
+  const int64_t items = s.capacity * s.heads;
+  if (items > (1LL << 31) - 1 - s.sms) return cudaErrorInvalidValue;
+  if (s.planned) {
+    char* at = reinterpret_cast<char*>(ws);
+    int* count = reinterpret_cast<int*>(at);
+    Entry* list = reinterpret_cast<Entry*>(at + 256);
+    Join* joins = reinterpret_cast<Join*>(at + 256 + s.list_bytes);
+    kv_prefill_plan_kernel<<<1, 1024, 0, stream>>>(p, list, joins, count, (int)s.capacity,
+                                                   s.slots, s.sms);
     count_launch();
-    e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     p.count = count;
     p.list = list;
+    p.joins = joins;
+    if (s.slots > 0) {
+      p.part_o = reinterpret_cast<float*>(at + 256 + s.list_bytes + s.join_bytes);
+      p.part_l =
+          reinterpret_cast<float*>(at + 256 + s.list_bytes + s.join_bytes + s.o_bytes);
+    }
   }
-  const int grid = (int)(items < sms ? items : sms);
+  const int grid = (int)(items < s.sms ? items : s.sms);
   return kv.f16 ? launch_type<F16>(qm, km, vm, p, kv.Dk, kv.Dv, grid, dev, stream)
                 : launch_type<Bf16>(qm, km, vm, p, kv.Dk, kv.Dv, grid, dev, stream);
 }

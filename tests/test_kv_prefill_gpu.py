@@ -104,6 +104,29 @@ def test_paged_chunks_after_a_prefix(cuda_dev, dtype, Hq, Hkv, Dk, Dv, hf):
     check_attention(out, lse, ref, dtype, dtype, "paged")
 
 
+@pytest.mark.parametrize("new,held,Hq,Hkv,causal", [
+    ([1], [5000], 4, 2, True), ([7, 1, 0, 30], [3000, 9000, 700, 2000], 8, 1, True),
+    ([200], [4300], 2, 2, True), ([40, 3], [1500, 1], 40, 1, False),
+    ([3000, 2], [2500, 1025], 2, 1, True)])
+def test_few_items_with_many_keys(cuda_dev, new, held, Hq, Hkv, causal):
+    """Too few items for the GPU: their keys are cut into pieces and joined.
+    (The last case has rows that see nothing in some pieces, or in none.)"""
+    gen = torch.Generator().manual_seed(sum(held))
+    kc, pt = paged_cache(held, Hkv, 64, torch.bfloat16, gen, spare_pages=5)
+    vc = torch.randn(kc.shape, generator=gen).to(torch.bfloat16)
+    q = (1.5 * torch.randn((sum(new), Hq, 64), generator=gen)).to(torch.bfloat16)
+    cq = _cu(new)
+    ref = _join([attend64(q[cq[b]:cq[b + 1]], rows_of(kc, pt, b, m), rows_of(vc, pt, b, m), 0.125,
+                          _limits(n, m, causal)) for b, (n, m) in enumerate(zip(new, held))])
+    d = [t.to(cuda_dev) for t in (q, kc, vc, cq)]
+    seq = torch.tensor(held, dtype=torch.int32, device=cuda_dev)
+    for dtype in (torch.bfloat16, torch.float32):
+        out, lse = tp.kv_prefill(*d, seq_lens=seq, page_table=pt.to(cuda_dev), scale=0.125,
+                                 causal=causal, out_dtype=dtype)
+        assert tp.device_status() == 0
+        check_attention(out, lse, ref, torch.bfloat16, dtype, "pieces")
+
+
 def test_a_neighbours_rows_are_not_used(cuda_dev):
     """Packed: a request's last tile holds its neighbour's first rows; what
     stands there (NaN, infinities) does not reach it."""
