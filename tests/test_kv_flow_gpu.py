@@ -107,7 +107,8 @@ def test_a_captured_decode_step(cuda_dev):
         assert torch.equal(kc, a_k) and torch.equal(vc, a_v)
         assert torch.equal(got[:3], want[:3]) and torch.equal(got_lse[:3], want_lse[:3])
         assert not got[3].any() and torch.all(torch.isneginf(got_lse[3]))
-        assert torch.equal(qr[3], was_q)
+        # bit by bit: the row was never written and may hold NaN, unequal to itself
+        assert torch.equal(qr[3].view(torch.int16), was_q.view(torch.int16))
     assert tp.device_status() == 0
 
 
