@@ -11,14 +11,16 @@
 // cuts leaves normalised partial results that the merge kernel joins by their
 // log-sum-exp.
 //
-// A block is one TMA producer warp and eight consumer warps over a ring of
+// A block is eight consumer warps and TMA producer warps over rings of
 // 64-token stages (K and V of one page of one key head, 128-byte swizzle).
 // The g query heads are the rows of one or more 16-row matrix products
 // (mma.sync m16n8k16: a page gives the tensor core too little work to gain
 // from TMEM accumulators; the copies are the limit).  Warps split rows (16
 // each, for g > 16) and then tokens; each keeps its own running maximum, sums
 // and accumulator in registers, so nothing in the loop waits for another
-// warp, and they meet once at the end of a (request, head) segment.
+// warp, and they meet once at the end of a (request, head) segment.  Up to 16
+// rows the consumers are two groups of four warps, each with its slice, its
+// ring and its producer: one group's segment end passes while the other reads.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -37,12 +39,12 @@ __device__ int g_kv_decode_status;
 
 constexpr int kPage = 64;
 constexpr int kConsumers = 8;                      // warps
-constexpr int kThreads = 32 * (kConsumers + 1);    // and the producer
+constexpr int kMergeScan = 2048;                   // most requests the merge sums up itself
 constexpr int kMaxRows = 128;                      // query heads of one row group
 constexpr int kMaxStages = 12;
 constexpr int kSegUnits = 3;  // 13 ragged requests of 16 heads: 94, 87, 71, 68, 68 us for 0 to 4
 constexpr int kSmemMax = 232448;
-constexpr int kMiscBytes = 2048;                   // barriers, stage counts, statistics
+constexpr int kMiscBytes = 2560;                   // barriers, stage counts, statistics
 
 struct Params {
   const uint16_t* q;
@@ -54,7 +56,7 @@ struct Params {
   int cap_rows;
   int B, Hq, Hkv, g, groups, rows;  // row groups per key head, rows of a group (<= 128)
   float scale_log2;
-  int ranges;                       // slices of the work (blocks)
+  int ranges;                       // slices of the work (one a group of warps)
   void* out;
   int out_dtype;
   int64_t o_sb, o_sh;
@@ -112,7 +114,7 @@ __device__ __forceinline__ bool seg_next(const Params& p, int range, Walk& w, Se
     const long long off = w.pos - w.base;
     s.b = w.b;
     s.len = len;
-    s.task = (int)(off / units);
+    s.task = off >> 32 ? (int)(off / units) : (int)((uint32_t)off / (uint32_t)units);
     const int u0 = (int)(off - (long long)s.task * units);
     const long long left = w.hi - w.pos;
     const int u1 = left < units - u0 ? u0 + (int)left : units;
@@ -181,50 +183,60 @@ __device__ __forceinline__ uint32_t tile_off(int row, int c16) {
 // DK, DV: head widths; RB: 16-row blocks of the row group (1, 2, 4, 8).
 template <typename T, int DK, int DV, int RB>
 struct Cfg {
+  static constexpr int kGroups = RB == 1 ? 2 : 1;        // of warps, each with a slice of its own
+  static constexpr int kWarps = kConsumers / kGroups;    // consumers of a group
+  static constexpr int kThreads = 32 * (kConsumers + kGroups);
   static constexpr int kK = kPage * DK * 2, kV = kPage * DV * 2;
   static constexpr int kStage = kK + kV;
-  static constexpr int kTS = kConsumers / RB;            // warps that share a row block
-  static constexpr int kAlt = RB == 1 ? 2 : 1;           // stages taken in turn by warp halves
-  static constexpr int kSlices = kTS / kAlt;             // token slices of a stage
-  static constexpr int kNT = kPage / kSlices;            // tokens of a slice
-  static constexpr int kJoin = kConsumers * 16 * (DV / 2) * 4;  // one half of the columns
-  static constexpr int kRing0 = (kSmemMax - 1024 - kMiscBytes - kJoin) / kStage;
-  static constexpr int kStages = kRing0 < kMaxStages ? kRing0 : kMaxStages;
-  static constexpr int kSmem = 1024 + kStages * kStage + kJoin + kMiscBytes;
-  static_assert(kStages >= 3 && kSmem <= kSmemMax, "shared memory");
+  static constexpr int kTS = kWarps / RB;                // warps that share a row block: token slices
+  static constexpr int kNT = kPage / kTS;                // tokens of a slice
+  static constexpr int kJoin = kWarps * 16 * (DV / 2) * 4;  // one half of the columns
+  static constexpr int kRing0 =
+      (kSmemMax - kMiscBytes - kGroups * kJoin) / kStage / kGroups;
+  static constexpr int kStages = kRing0 < kMaxStages ? kRing0 : kMaxStages;  // of a group
+  static constexpr int kSmem = kGroups * (kStages * kStage + kJoin) + kMiscBytes;
+  static_assert(kStages >= 2 && kSmem <= kSmemMax, "shared memory");
 };
 
-struct Misc {  // in shared memory
+struct GroupMisc {  // in shared memory
   unsigned long long full[kMaxStages], empty[kMaxStages];
   int nv[kMaxStages];  // valid tokens of a stage
-  int abort_flag, b0;
-  long long base0, total;
-  long long warp_sum[kConsumers + 1];
+  int b0;
+  long long base0;
+};
+struct Misc {
+  GroupMisc group[2];
+  int abort_flag;
+  long long warp_sum[kConsumers + 2];
   float stat[kConsumers][16][3];  // m, sum of rounded weights, sum of exact weights
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc shared memory");
 
 template <typename T, int DK, int DV, int RB>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<T, DK, DV, RB>::kThreads, 1)
 kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const Params p) {
   using C = Cfg<T, DK, DV, RB>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem =
-      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sbase = smem_addr(smem);
-  float* join = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
-  Misc& ms = *reinterpret_cast<Misc*>(smem + C::kStages * C::kStage + C::kJoin);
-  volatile int* abort_flag = &ms.abort_flag;
+  extern __shared__ __align__(1024) uint8_t smem[];  // swizzled tiles begin on 1 KB
+  Misc& all = *reinterpret_cast<Misc*>(smem + C::kGroups * (C::kStages * C::kStage + C::kJoin));
+  volatile int* abort_flag = &all.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int range = blockIdx.x;
+  // consumers of group 0, of group 1, then the producers
+  const bool produces = warp >= kConsumers;
+  const int group = produces ? warp - kConsumers : warp / C::kWarps;
+  const int range = blockIdx.x * C::kGroups + group;
+  GroupMisc& ms = all.group[group];
+  const uint32_t sbase = smem_addr(smem + group * C::kStages * C::kStage);
+  float* join = reinterpret_cast<float*>(smem + C::kGroups * C::kStages * C::kStage +
+                                         group * C::kJoin);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(smem_addr(&ms.full[i]), 1);
-      mbar_init(smem_addr(&ms.empty[i]), kConsumers / C::kAlt);
-    }
-    ms.abort_flag = 0;
+    for (int g = 0; g < C::kGroups; ++g)
+      for (int i = 0; i < C::kStages; ++i) {
+        mbar_init(smem_addr(&all.group[g].full[i]), 1);
+        mbar_init(smem_addr(&all.group[g].empty[i]), C::kWarps);
+      }
+    all.abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kConsumers && lane == 0) {
@@ -235,7 +247,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // units before each thread's run of requests, and the request where this
   // block's slice begins
-  const int run = (p.B + kThreads - 1) / kThreads;
+  const int run = (p.B + C::kThreads - 1) / C::kThreads;
   const int b_lo = min(p.B, (int)threadIdx.x * run), b_hi = min(p.B, b_lo + run);
   long long mine = 0;
   for (int b = b_lo; b < b_hi; ++b) mine += req_units(p, b);
@@ -245,36 +257,38 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const long long v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) ms.warp_sum[warp] = incl;
+  if (lane == 31) all.warp_sum[warp] = incl;
   __syncthreads();
   long long before = incl - mine, total = 0;
 #pragma unroll
-  for (int i = 0; i <= kConsumers; ++i) {
-    if (i < warp) before += ms.warp_sum[i];
-    total += ms.warp_sum[i];
+  for (int i = 0; i < kConsumers + C::kGroups; ++i) {
+    if (i < warp) before += all.warp_sum[i];
+    total += all.warp_sum[i];
   }
-  // no slice is empty: where there are fewer units than blocks, the first
-  // `slices` blocks take one each
+  // no slice is empty: where there are fewer units than groups, the first
+  // `slices` groups take one each
   const long long slices = total < p.ranges ? total : p.ranges;
-  Walk w;
-  w.pos = w.hi = total;
-  w.emitted = 0;
-  if (range < slices) {
-    w.pos = total * range / slices;
-    w.hi = total * (range + 1) / slices;
-  }
-  if (w.pos >= before && w.pos < before + mine) {
-    long long base = before;
-    int b = b_lo;
-    for (;; ++b) {
-      const long long n = req_units(p, b);
-      if (w.pos < base + n) break;
-      base += n;
+  auto slice_begin = [&](int r) { return r < slices ? total * r / slices : total; };
+#pragma unroll
+  for (int g = 0; g < C::kGroups; ++g) {
+    const long long at = slice_begin(blockIdx.x * C::kGroups + g);
+    if (at >= before && at < before + mine) {
+      long long base = before;
+      int b = b_lo;
+      for (;; ++b) {
+        const long long n = req_units(p, b);
+        if (at < base + n) break;
+        base += n;
+      }
+      all.group[g].b0 = b;
+      all.group[g].base0 = base;
     }
-    ms.b0 = b;
-    ms.base0 = base;
   }
-  if (range == 0) {  // for the merge
+  Walk w;
+  w.pos = slice_begin(range);
+  w.hi = slice_begin(range + 1);
+  w.emitted = 0;
+  if (blockIdx.x == 0 && p.B > kMergeScan) {  // for the merge
     long long base = before;
     for (int b = b_lo; b < b_hi; ++b) {
       p.base[b] = base;
@@ -289,7 +303,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   Segment s;
   uint32_t n = 0;  // stages so far
 
-  if (warp == kConsumers) {  // ------------------------------------------------ producer
+  if (produces) {  // ------------------------------------------------------- producer
     while (seg_next(p, range, w, s)) {
       const int hk = s.task / p.groups;
       int win = 0;  // lane i: page id of page w0 + i
@@ -327,10 +341,12 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   }
 
   // ------------------------------------------------------------------ consumers
-  const int rb = warp % RB, ts = warp / RB;
-  const int turn = ts / C::kSlices, slice = ts % C::kSlices;
+  const int gw = warp - group * C::kWarps, tid = gw * 32 + lane;  // within the group
+  const int rb = gw % RB, slice = gw / RB;
   const int r = lane >> 2, c2 = (lane & 3) * 2;
   const int t0 = slice * C::kNT;
+  const uint32_t bar_id = 1 + group;
+  float(*stat)[16][3] = all.stat + group * C::kWarps;  // of the group's warps
   bool dead = false;  // a wait gave up: no more pages, but the block's barriers are kept
   // the queries as A fragments: rows r and r + 8 of this row block
   uint32_t qf[DK / 16][4];
@@ -368,7 +384,6 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     float le[2] = {0.f, 0.f};             // sum of the f32 weights: the log-sum-exp
 
     for (int pg = dead ? s.page1 : s.page0; pg < s.page1; ++pg, ++n) {
-      if (C::kAlt == 2 && (int)(n & 1) != turn) continue;
       const int slot = n % C::kStages;
       int ok = 1;
       if (lane == 0)
@@ -475,141 +490,193 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         le[j] += __shfl_xor_sync(0xffffffffu, le[j], x);
       }
       if ((lane & 3) == 0) {
-        float* st = ms.stat[warp][r + 8 * j];
+        float* st = stat[gw][r + 8 * j];
         st[0] = m[j];
         st[1] = lr[j];
         st[2] = le[j];
       }
     }
-    named_bar_sync(1, 32 * kConsumers);
+    named_bar_sync(bar_id, 32 * C::kWarps);
+    // this warp's factor in its rows' results, and the rows' log-sum-exp
     float f[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float top = -INFINITY;
+      const int ri = r + 8 * j;
+      float top = -INFINITY, slr = 0.f, sle = 0.f;
 #pragma unroll
-      for (int x = 0; x < C::kTS; ++x) top = fmaxf(top, ms.stat[x * RB + rb][r + 8 * j][0]);
-      f[j] = m[j] == -INFINITY ? 0.f : ex2(m[j] - top);
+      for (int x = 0; x < C::kTS; ++x) top = fmaxf(top, stat[x * RB + rb][ri][0]);
+#pragma unroll
+      for (int x = 0; x < C::kTS; ++x) {
+        const float* st = stat[x * RB + rb][ri];
+        const float fx = st[0] == -INFINITY ? 0.f : ex2(st[0] - top);
+        slr += st[1] * fx;
+        sle += st[2] * fx;
+      }
+      const float inv = slr > 0.f ? 1.f / slr : (slr == 0.f ? 0.f : NAN);
+      f[j] = m[j] == -INFINITY ? 0.f : ex2(m[j] - top) * inv;
+      const int rw = rb * 16 + ri;
+      if (slice == 0 && (lane & 3) == 0 && rw < nrows) {
+        const float l = sle > 0.f ? (top + log2f(sle)) * kLn2 : (sle == 0.f ? -INFINITY : NAN);
+        if (!s.complete)
+          p.part_l[(int64_t)s.slot * p.rows + rw] = l;
+        else if (p.lse)
+          p.lse[(int64_t)s.b * p.l_sb + (int64_t)(h0 + rw) * p.l_sh] = l;
+      }
     }
-    // all columns at once where the rows above 8 are not used, else in halves
+    // all columns at once where the rows above 8 are not used, else in halves;
+    // 8-column blocks change places by row, so that the rows' stores meet in
+    // no bank
     const bool narrow = RB == 1 && nrows <= 8;
     const int passes = narrow ? 1 : 2, rows_w = narrow ? 8 : 16;
     const int cols = DV / passes;
     for (int pass = 0; pass < passes; ++pass) {
-      if (pass) named_bar_sync(1, 32 * kConsumers);
-      float* d = join + (warp * rows_w + r) * cols + c2;
+      if (pass) named_bar_sync(bar_id, 32 * C::kWarps);
+      float* d = join + (gw * rows_w + r) * cols;
 #pragma unroll
       for (int i = 0; i < DV / 8; ++i) {
         const int at = 8 * i - pass * cols;
         if (at < 0 || at >= cols) continue;
-        *reinterpret_cast<float2*>(d + at) = make_float2(o[i][0] * f[0], o[i][1] * f[0]);
+        const int c = (at ^ ((r & 3) << 3)) + c2;
+        *reinterpret_cast<float2*>(d + c) = make_float2(o[i][0] * f[0], o[i][1] * f[0]);
         if (!narrow)
-          *reinterpret_cast<float2*>(d + 8 * cols + at) =
+          *reinterpret_cast<float2*>(d + 8 * cols + c) =
               make_float2(o[i][2] * f[1], o[i][3] * f[1]);
       }
-      named_bar_sync(1, 32 * kConsumers);
-      for (int e = threadIdx.x; e < nrows * (cols / 2); e += 32 * kConsumers) {
-        const int rw = e / (cols / 2), c = 2 * (e - rw * (cols / 2));
+      named_bar_sync(bar_id, 32 * C::kWarps);
+      for (int e = tid; e < nrows * (cols / 4); e += 32 * C::kWarps) {
+        const int rw = e / (cols / 4), c = 4 * (e - rw * (cols / 4));
         const int blk = rw >> 4, ri = rw & 15;
-        float top = -INFINITY, slr = 0.f, sle = 0.f, v0 = 0.f, v1 = 0.f;
-#pragma unroll
-        for (int x = 0; x < C::kTS; ++x) top = fmaxf(top, ms.stat[x * RB + blk][ri][0]);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int x = 0; x < C::kTS; ++x) {
-          const float* st = ms.stat[x * RB + blk][ri];
-          const float fx = st[0] == -INFINITY ? 0.f : ex2(st[0] - top);
-          slr += st[1] * fx;
-          sle += st[2] * fx;
-          const float2 v = *reinterpret_cast<const float2*>(
-              join + ((x * RB + blk) * rows_w + ri) * cols + c);
-          v0 += v.x;
-          v1 += v.y;
+          const float4 y = *reinterpret_cast<const float4*>(
+              join + ((x * RB + blk) * rows_w + ri) * cols + (c ^ ((ri & 3) << 3)));
+          v.x += y.x;
+          v.y += y.y;
+          v.z += y.z;
+          v.w += y.w;
         }
-        const float inv = slr > 0.f ? 1.f / slr : (slr == 0.f ? 0.f : NAN);
-        v0 *= inv;
-        v1 *= inv;
         const int col = pass * cols + c;
-        if (s.complete)
-          store_out(p, s.b, h0 + rw, col, v0, v1);
-        else
-          *reinterpret_cast<float2*>(p.part_o + ((int64_t)s.slot * p.rows + rw) * DV + col) =
-              make_float2(v0, v1);
-        if (col == 0) {
-          const float l = sle > 0.f ? (top + log2f(sle)) * kLn2 : (sle == 0.f ? -INFINITY : NAN);
-          if (!s.complete)
-            p.part_l[(int64_t)s.slot * p.rows + rw] = l;
-          else if (p.lse)
-            p.lse[(int64_t)s.b * p.l_sb + (int64_t)(h0 + rw) * p.l_sh] = l;
+        if (s.complete) {
+          store_out(p, s.b, h0 + rw, col, v.x, v.y);
+          store_out(p, s.b, h0 + rw, col + 2, v.z, v.w);
+        } else {
+          *reinterpret_cast<float4*>(p.part_o + ((int64_t)s.slot * p.rows + rw) * DV + col) = v;
         }
       }
     }
-    named_bar_sync(1, 32 * kConsumers);
+    named_bar_sync(bar_id, 32 * C::kWarps);
   }
 }
 
 // ---------------------------------------------------------------- merge
-// One block per (request, key head, row group), one warp per row at a time.
-// Tasks inside one slice are final already; requests without tokens get
-// out = 0 and lse = -inf here.
+// A warp per (request, head).  Tasks inside one slice are final already;
+// requests without tokens get out = 0 and lse = -inf here.  The lanes hold the
+// pieces' log-sum-exp, 32 at a time, so the pieces' rows are read without
+// waiting for one another.
 constexpr int kMergeWarps = 4;
 
+// What depends on the lengths alone is found before the wait for the decode
+// kernel, whose end this kernel's start overlaps; for very many requests the
+// units before each are read from that kernel's list instead of being summed.
 template <int DV>
 __global__ void __launch_bounds__(32 * kMergeWarps) kv_decode_merge_kernel(const Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ long long sums[2][kMergeWarps];
   const int tasks = p.Hkv * p.groups;
   const int b = blockIdx.x / tasks, task = blockIdx.x - b * tasks;
   const int hk = task / p.groups, rg = task - hk * p.groups;
   const int h0 = hk * p.g + rg * kMaxRows, nrows = min(p.g - rg * kMaxRows, kMaxRows);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long base = p.base[b], total = p.base[p.B];
-  const long long units = (p.base[b + 1] - base) / tasks;
-  constexpr int kV = DV / 32;  // values of a lane
-  if (units == 0) {
-    for (int rw = warp; rw < nrows; rw += kMergeWarps) {
-#pragma unroll
-      for (int i = 0; i < kV; i += 2) store_out(p, b, h0 + rw, lane * kV + i, 0.f, 0.f);
-      if (p.lse && lane == 0) p.lse[(int64_t)b * p.l_sb + (int64_t)(h0 + rw) * p.l_sh] = -INFINITY;
+  const int rw = blockIdx.y * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  long long base = 0, total = 0;
+  if (p.B <= kMergeScan) {
+    for (int i = threadIdx.x; i < p.B; i += 32 * kMergeWarps) {
+      const long long u = req_units(p, i);
+      total += u;
+      if (i < b) base += u;
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      base += __shfl_xor_sync(0xffffffffu, base, o);
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane == 0) {
+      sums[0][threadIdx.x >> 5] = base;
+      sums[1][threadIdx.x >> 5] = total;
+    }
+    __syncthreads();
+    base = total = 0;
+#pragma unroll
+    for (int i = 0; i < kMergeWarps; ++i) {
+      base += sums[0][i];
+      total += sums[1][i];
+    }
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    base = p.base[b];
+    total = p.base[p.B];
+  }
+  const int pages = req_pages(p, b);
+  constexpr int kV = DV / 32;  // values of a lane
+  // the task's pages are units [u0, u1)
+  const long long start = base + (long long)(pages + kSegUnits) * task, u0 = start + kSegUnits,
+                  u1 = u0 + pages;
+  const long long slices = total < p.ranges ? total : p.ranges;
+  int r0 = 0, r1 = 0, first = 0;
+  if (pages > 0) {
+    if (total < (1 << 22)) {  // times at most 2^9 slices
+      const uint32_t t = (uint32_t)total, sl = (uint32_t)slices;
+      r0 = (int)((((uint32_t)u0 + 1) * sl - 1) / t);
+      r1 = (int)(((uint32_t)u1 * sl - 1) / t);
+      first = 2 * r0 + (t * (uint32_t)r0 / sl >= (uint32_t)start ? 0 : 1);
+    } else {
+      r0 = (int)(((u0 + 1) * slices - 1) / total);
+      r1 = (int)((u1 * slices - 1) / total);
+      // the task is slice r0's first segment only where the slice begins with
+      // it (the unit before a task is a page of another one)
+      first = 2 * r0 + (total * r0 / slices >= start ? 0 : 1);
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (rw >= nrows) return;
+  if (pages == 0) {
+#pragma unroll
+    for (int i = 0; i < kV; i += 2) store_out(p, b, h0 + rw, lane * kV + i, 0.f, 0.f);
+    if (p.lse && lane == 0) p.lse[(int64_t)b * p.l_sb + (int64_t)(h0 + rw) * p.l_sh] = -INFINITY;
     return;
   }
-  // the task's pages are units [u0, u1)
-  const long long start = base + units * task, u0 = start + kSegUnits, u1 = start + units;
-  const long long slices = total < p.ranges ? total : p.ranges;
-  const int r0 = (int)(((u0 + 1) * slices - 1) / total);
-  const int r1 = (int)((u1 * slices - 1) / total);
   if (r0 == r1) return;
-  // the task is slice r0's first segment only where the slice begins with it
-  // (the unit before a task is a page of another one)
-  const int first = 2 * r0 + (total * r0 / slices >= start ? 0 : 1);
-  for (int rw = warp; rw < nrows; rw += kMergeWarps) {
-    float top = -INFINITY;
-    for (int x = r0 + lane; x <= r1; x += 32)
-      top = fmaxf(top, p.part_l[(int64_t)(x == r0 ? first : 2 * x) * p.rows + rw]);
+  auto slot_of = [&](int x) { return (int64_t)(x == r0 ? first : 2 * x) * p.rows + rw; };
+  float top = -INFINITY;
+  for (int x = r0 + lane; x <= r1; x += 32) top = fmaxf(top, p.part_l[slot_of(x)]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc[kV];
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, acc[kV];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) acc[i] = 0.f;
-    for (int x = r0; x <= r1; ++x) {
-      const int64_t slot = x == r0 ? first : 2 * x;
-      const float wgt = expf(p.part_l[slot * p.rows + rw] - ref);
+  for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+  for (int x0 = r0; x0 <= r1; x0 += 32) {
+    const int n = min(32, r1 - x0 + 1);
+    const float mine = lane < n ? expf(p.part_l[slot_of(x0 + lane)] - ref) : 0.f;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float wgt = __shfl_sync(0xffffffffu, mine, i);
+      const float* src = p.part_o + slot_of(x0 + i) * DV + lane * kV;
       sum += wgt;
-      const float* src = p.part_o + (slot * p.rows + rw) * DV + lane * kV;
 #pragma unroll
-      for (int i = 0; i < kV; i += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + i);
-        acc[i] = fmaf(wgt, v.x, acc[i]);
-        acc[i + 1] = fmaf(wgt, v.y, acc[i + 1]);
+      for (int k = 0; k < kV; k += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(src + k);
+        acc[k] = fmaf(wgt, v.x, acc[k]);
+        acc[k + 1] = fmaf(wgt, v.y, acc[k + 1]);
       }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int i = 0; i < kV; i += 2)
-      store_out(p, b, h0 + rw, lane * kV + i, acc[i] * inv, acc[i + 1] * inv);
-    if (p.lse && lane == 0)
-      p.lse[(int64_t)b * p.l_sb + (int64_t)(h0 + rw) * p.l_sh] =
-          sum > 0.f ? ref + logf(sum) : -INFINITY;
   }
+  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : NAN);
+#pragma unroll
+  for (int i = 0; i < kV; i += 2)
+    store_out(p, b, h0 + rw, lane * kV + i, acc[i] * inv, acc[i + 1] * inv);
+  if (p.lse && lane == 0)
+    p.lse[(int64_t)b * p.l_sb + (int64_t)(h0 + rw) * p.l_sh] =
+        sum > 0.f ? ref + logf(sum) : (sum == 0.f ? -INFINITY : NAN);
 }
 
 // ---------------------------------------------------------------- host side
@@ -629,12 +696,14 @@ cudaError_t launch_rb(const CUtensorMap& km, const CUtensorMap& vm, const Params
       ready |= 1ull << dev;
     }
   }
-  kv_decode_kernel<T, DK, DV, RB><<<p.ranges, kThreads, C::kSmem, stream>>>(km, vm, p);
+  kv_decode_kernel<T, DK, DV, RB>
+      <<<(p.ranges + C::kGroups - 1) / C::kGroups, C::kThreads, C::kSmem, stream>>>(km, vm, p);
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.groups));
+  cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.groups),
+                     (unsigned)((p.rows + kMergeWarps - 1) / kMergeWarps));
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -670,8 +739,8 @@ struct Schedule {
   size_t base_bytes, o_bytes, l_bytes;
 };
 
-// One slice per SM (a block takes the SM's shared memory), fewer where the
-// caches cannot hold that many pages.
+// One block per SM (it takes the SM's shared memory), and in it a slice for
+// each group of warps; fewer where the caches cannot hold that many pages.
 Schedule schedule(const KvDecodeProblem& p, int device) {
   Schedule s;
   s.g = p.Hq / p.kv.Hkv;
@@ -685,7 +754,8 @@ Schedule schedule(const KvDecodeProblem& p, int device) {
   }
   const int64_t pages = (p.kv.cap_rows + kPage - 1) / kPage;
   const int64_t units = (pages + kSegUnits) * p.B * p.kv.Hkv * s.groups;
-  s.ranges = (int)(units < sms ? (units > 0 ? units : 1) : sms);
+  const int most = s.rows <= 16 ? 2 * sms : sms;
+  s.ranges = (int)(units < most ? (units > 0 ? units : 1) : most);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   s.base_bytes = up((size_t)(p.B + 1) * sizeof(long long));
   s.o_bytes = up((size_t)2 * s.ranges * s.rows * p.kv.Dv * sizeof(float));
