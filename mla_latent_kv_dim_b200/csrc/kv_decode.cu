@@ -39,7 +39,6 @@ __device__ int g_kv_decode_status;
 
 constexpr int kPage = 64;
 constexpr int kConsumers = 8;                      // warps
-constexpr int kMergeScan = 2048;                   // most requests the merge sums up itself
 constexpr int kMaxRows = 128;                      // query heads of one row group
 constexpr int kMaxStages = 12;
 constexpr int kSegUnits = 3;  // 13 ragged requests of 16 heads: 94, 87, 71, 68, 68 us for 0 to 4
@@ -62,7 +61,8 @@ struct Params {
   int64_t o_sb, o_sh;
   float* lse;
   int64_t l_sb, l_sh;
-  long long* base;  // [B + 1] units before each request
+  int4* cut;        // [ranges] the task that slice r begins and does not end:
+                    // (first slot, pieces, request, task), pieces 0: none
   float* part_o;    // [2 ranges, rows, Dv]
   float* part_l;    // [2 ranges, rows]
 };
@@ -96,6 +96,7 @@ struct Walk {
 struct Segment {
   int b, task, page0, page1, len;
   int complete, slot;
+  long long end;   // unit behind the task
 };
 
 // The slice's next segment: a slice cuts at most its first and its last, so
@@ -124,6 +125,7 @@ __device__ __forceinline__ bool seg_next(const Params& p, int range, Walk& w, Se
     if (s.page1 <= s.page0) continue;  // the slice ends in the fixed work
     s.complete = s.page0 == 0 && s.page1 == pages;
     s.slot = 2 * range + (w.emitted ? 1 : 0);
+    s.end = w.base + (long long)(s.task + 1) * units;
     ++w.emitted;
     return true;
   }
@@ -288,16 +290,21 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   w.pos = slice_begin(range);
   w.hi = slice_begin(range + 1);
   w.emitted = 0;
-  if (blockIdx.x == 0 && p.B > kMergeScan) {  // for the merge
-    long long base = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      p.base[b] = base;
-      base += req_units(p, b);
+  // requests without tokens
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (req_pages(p, b) > 0) continue;
+    for (int e = threadIdx.x; e < p.Hq * (DV / 2); e += C::kThreads) {
+      const int h = e / (DV / 2), c = 2 * (e - h * (DV / 2));
+      store_out(p, b, h, c, 0.f, 0.f);
+      if (c == 0 && p.lse) p.lse[(int64_t)b * p.l_sb + (int64_t)h * p.l_sh] = -INFINITY;
     }
-    if (threadIdx.x == 0) p.base[p.B] = total;
   }
   __syncthreads();
-  if (w.pos >= w.hi) return;
+  if (w.pos >= w.hi) {
+    if (!produces && warp == group * C::kWarps && lane == 0 && range < p.ranges)
+      p.cut[range] = make_int4(0, 0, 0, 0);
+    return;
+  }
   w.b = ms.b0;
   w.base = ms.base0;
   Segment s;
@@ -368,12 +375,20 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   Segment nx;
   bool more = seg_next(p, range, w, nx);
   if (more) load_q(nx);
+  if (tid == 0) p.cut[range] = make_int4(0, 0, 0, 0);
   while (more) {
     s = nx;
     more = seg_next(p, range, w, nx);
     const int hk = s.task / p.groups, rg = s.task - hk * p.groups;
     const int h0 = hk * p.g + rg * kMaxRows;            // first head of the row group
     const int nrows = min(p.g - rg * kMaxRows, kMaxRows);
+    if (tid == 0 && !s.complete && s.page0 == 0) {
+      // the slice with the task's last page
+      const int last = total < (1 << 22)  // times at most 2^9 slices
+                           ? (int)(((uint32_t)s.end * (uint32_t)slices - 1) / (uint32_t)total)
+                           : (int)((s.end * slices - 1) / total);
+      p.cut[range] = make_int4(s.slot, last - range + 1, s.b, s.task);
+    }
     float o[DV / 8][4];
 #pragma unroll
     for (int i = 0; i < DV / 8; ++i)
@@ -570,113 +585,50 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 }
 
 // ---------------------------------------------------------------- merge
-// A warp per (request, head).  Tasks inside one slice are final already;
-// requests without tokens get out = 0 and lse = -inf here.  The lanes hold the
-// pieces' log-sum-exp, 32 at a time, so the pieces' rows are read without
-// waiting for one another.
+// Joins the pieces of the tasks that a slice's border cuts: a warp per row, a
+// block column per slice, which says what it began and did not end.  The
+// following pieces are the first segments of the following slices.  (The code
+// is short on purpose: fetching instructions is most of a small launch.)
 constexpr int kMergeWarps = 4;
 
-// What depends on the lengths alone is found before the wait for the decode
-// kernel, whose end this kernel's start overlaps; for very many requests the
-// units before each are read from that kernel's list instead of being summed.
 template <int DV>
 __global__ void __launch_bounds__(32 * kMergeWarps) kv_decode_merge_kernel(const Params p) {
-  __shared__ long long sums[2][kMergeWarps];
-  const int tasks = p.Hkv * p.groups;
-  const int b = blockIdx.x / tasks, task = blockIdx.x - b * tasks;
-  const int hk = task / p.groups, rg = task - hk * p.groups;
-  const int h0 = hk * p.g + rg * kMaxRows, nrows = min(p.g - rg * kMaxRows, kMaxRows);
   const int rw = blockIdx.y * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  long long base = 0, total = 0;
-  if (p.B <= kMergeScan) {
-    for (int i = threadIdx.x; i < p.B; i += 32 * kMergeWarps) {
-      const long long u = req_units(p, i);
-      total += u;
-      if (i < b) base += u;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      base += __shfl_xor_sync(0xffffffffu, base, o);
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-    }
-    if (lane == 0) {
-      sums[0][threadIdx.x >> 5] = base;
-      sums[1][threadIdx.x >> 5] = total;
-    }
-    __syncthreads();
-    base = total = 0;
-#pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) {
-      base += sums[0][i];
-      total += sums[1][i];
-    }
-  } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    base = p.base[b];
-    total = p.base[p.B];
-  }
-  const int pages = req_pages(p, b);
-  constexpr int kV = DV / 32;  // values of a lane
-  // the task's pages are units [u0, u1)
-  const long long start = base + (long long)(pages + kSegUnits) * task, u0 = start + kSegUnits,
-                  u1 = u0 + pages;
-  const long long slices = total < p.ranges ? total : p.ranges;
-  int r0 = 0, r1 = 0, first = 0;
-  if (pages > 0) {
-    if (total < (1 << 22)) {  // times at most 2^9 slices
-      const uint32_t t = (uint32_t)total, sl = (uint32_t)slices;
-      r0 = (int)((((uint32_t)u0 + 1) * sl - 1) / t);
-      r1 = (int)(((uint32_t)u1 * sl - 1) / t);
-      first = 2 * r0 + (t * (uint32_t)r0 / sl >= (uint32_t)start ? 0 : 1);
-    } else {
-      r0 = (int)(((u0 + 1) * slices - 1) / total);
-      r1 = (int)((u1 * slices - 1) / total);
-      // the task is slice r0's first segment only where the slice begins with
-      // it (the unit before a task is a page of another one)
-      first = 2 * r0 + (total * r0 / slices >= start ? 0 : 1);
-    }
-  }
+  const int range = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (rw >= nrows) return;
-  if (pages == 0) {
-#pragma unroll
-    for (int i = 0; i < kV; i += 2) store_out(p, b, h0 + rw, lane * kV + i, 0.f, 0.f);
-    if (p.lse && lane == 0) p.lse[(int64_t)b * p.l_sb + (int64_t)(h0 + rw) * p.l_sh] = -INFINITY;
-    return;
-  }
-  if (r0 == r1) return;
-  auto slot_of = [&](int x) { return (int64_t)(x == r0 ? first : 2 * x) * p.rows + rw; };
+  const int4 cut = p.cut[range];
+  const int n = cut.y, hk = cut.w / p.groups, rg = cut.w - hk * p.groups;
+  if (n == 0 || rw >= min(p.g - rg * kMaxRows, kMaxRows)) return;
+  auto row_of = [&](int i) { return (i ? 2 * (range + i) : cut.x) * p.rows + rw; };
   float top = -INFINITY;
-  for (int x = r0 + lane; x <= r1; x += 32) top = fmaxf(top, p.part_l[slot_of(x)]);
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.part_l[row_of(i)]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float ref = top == -INFINITY ? 0.f : top;
+  constexpr int kV = DV / 32;  // values of a lane
   float sum = 0.f, acc[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) acc[i] = 0.f;
-  for (int x0 = r0; x0 <= r1; x0 += 32) {
-    const int n = min(32, r1 - x0 + 1);
-    const float mine = lane < n ? expf(p.part_l[slot_of(x0 + lane)] - ref) : 0.f;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float wgt = __shfl_sync(0xffffffffu, mine, i);
-      const float* src = p.part_o + slot_of(x0 + i) * DV + lane * kV;
-      sum += wgt;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float wgt = ex2((p.part_l[row_of(i)] - ref) * kLog2e);
+    const float* src = p.part_o + (int64_t)row_of(i) * DV + lane * kV;
+    sum += wgt;
 #pragma unroll
-      for (int k = 0; k < kV; k += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + k);
-        acc[k] = fmaf(wgt, v.x, acc[k]);
-        acc[k + 1] = fmaf(wgt, v.y, acc[k + 1]);
-      }
+    for (int k = 0; k < kV; k += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(src + k);
+      acc[k] = fmaf(wgt, v.x, acc[k]);
+      acc[k + 1] = fmaf(wgt, v.y, acc[k + 1]);
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : NAN);
+  const int h = hk * p.g + rg * kMaxRows + rw;
 #pragma unroll
   for (int i = 0; i < kV; i += 2)
-    store_out(p, b, h0 + rw, lane * kV + i, acc[i] * inv, acc[i + 1] * inv);
+    store_out(p, cut.z, h, lane * kV + i, acc[i] * inv, acc[i + 1] * inv);
   if (p.lse && lane == 0)
-    p.lse[(int64_t)b * p.l_sb + (int64_t)(h0 + rw) * p.l_sh] =
-        sum > 0.f ? ref + logf(sum) : (sum == 0.f ? -INFINITY : NAN);
+    p.lse[(int64_t)cut.z * p.l_sb + (int64_t)h * p.l_sh] =
+        sum > 0.f ? ref + log2f(sum) * kLn2 : (sum == 0.f ? -INFINITY : NAN);
 }
 
 // ---------------------------------------------------------------- host side
@@ -702,7 +654,7 @@ cudaError_t launch_rb(const CUtensorMap& km, const CUtensorMap& vm, const Params
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.groups),
+  cfg.gridDim = dim3((unsigned)p.ranges,
                      (unsigned)((p.rows + kMergeWarps - 1) / kMergeWarps));
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = stream;
@@ -736,7 +688,7 @@ cudaError_t launch_type(const CUtensorMap& km, const CUtensorMap& vm, const Para
 
 struct Schedule {
   int g, groups, rows, ranges;
-  size_t base_bytes, o_bytes, l_bytes;
+  size_t cut_bytes, o_bytes, l_bytes;
 };
 
 // One block per SM (it takes the SM's shared memory), and in it a slice for
@@ -757,7 +709,7 @@ Schedule schedule(const KvDecodeProblem& p, int device) {
   const int most = s.rows <= 16 ? 2 * sms : sms;
   s.ranges = (int)(units < most ? (units > 0 ? units : 1) : most);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  s.base_bytes = up((size_t)(p.B + 1) * sizeof(long long));
+  s.cut_bytes = up((size_t)s.ranges * sizeof(int4));
   s.o_bytes = up((size_t)2 * s.ranges * s.rows * p.kv.Dv * sizeof(float));
   s.l_bytes = up((size_t)2 * s.ranges * s.rows * sizeof(float));
   return s;
@@ -771,7 +723,7 @@ bool kv_head_dims_supported(int Dk, int Dv) {
 
 size_t kv_decode_workspace_bytes(const KvDecodeProblem& p, int device) {
   const Schedule s = schedule(p, device);
-  return s.base_bytes + s.o_bytes + s.l_bytes;
+  return s.cut_bytes + s.o_bytes + s.l_bytes;
 }
 
 cudaError_t launch_kv_decode(const KvDecodeProblem& dp, void* ws, cudaStream_t stream) {
@@ -811,9 +763,9 @@ cudaError_t launch_kv_decode(const KvDecodeProblem& dp, void* ws, cudaStream_t s
   p.l_sb = dp.l_sb;
   p.l_sh = dp.l_sh;
   char* at = reinterpret_cast<char*>(ws);
-  p.base = reinterpret_cast<long long*>(at);
-  p.part_o = reinterpret_cast<float*>(at + s.base_bytes);
-  p.part_l = reinterpret_cast<float*>(at + s.base_bytes + s.o_bytes);
+  p.cut = reinterpret_cast<int4*>(at);
+  p.part_o = reinterpret_cast<float*>(at + s.cut_bytes);
+  p.part_l = reinterpret_cast<float*>(at + s.cut_bytes + s.o_bytes);
   return kv.f16 ? launch_type<F16>(km, vm, p, kv.Dk, kv.Dv, dev, stream)
                 : launch_type<Bf16>(km, vm, p, kv.Dk, kv.Dv, dev, stream);
 }

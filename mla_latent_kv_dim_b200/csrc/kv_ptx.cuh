@@ -17,6 +17,7 @@ namespace kvx {
 using namespace ptx;
 
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
 constexpr long long kTimeoutCycles = 4000000000LL;  // about 2 s at full clock
 constexpr uint32_t kWaitSleepNs = 100000;           // suspend hint of one barrier poll
 
