@@ -310,6 +310,8 @@ __device__ void qk_issuer(const Params& p, const int t, const CUtensorMap* qm, u
   constexpr uint32_t kC = kChunk >> 4, kT = C::kKV >> 4;
   const uint32_t q_lo = (uint32_t)dQ, k_lo = (uint32_t)dK, hi = (uint32_t)(dK >> 32);
   const uint32_t tS = tmem + kColS + kRows * t;
+  // a negative scale: bit 13 negates A, so that the maximum is still a maximum
+  const uint32_t idesc = C::idesc(kKeys, false) | (p.negate ? 1u << 13 : 0u);
   const uint32_t q_full = smem_addr(&ms.q_full[t]), q_empty = smem_addr(&ms.q_empty[t]);
   auto wait = [&](uint32_t bar, uint32_t parity) {
     return wait_bar(bar, parity, abort_flag, &g_kv_prefill_status);
@@ -343,7 +345,7 @@ __device__ void qk_issuer(const Params& p, const int t, const CUtensorMap* qm, u
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_ss(dS, q_lo + 2 * c * kC + 2 * k, hi, k0 + c * kC + 2 * k, hi,
-                   C::idesc(kKeys, false), (c | k) != 0);
+                   idesc, (c | k) != 0);
         commit(smem_addr(&ms.s_full[t][buf]));
         if (++slot == C::kRing) {
           slot = 0;
@@ -442,6 +444,21 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
       if (!wait(ms.s_full[t][buf], (cnt >> 1) & 1)) return;
       tc_fence_after();
       release(tiles + j);
+      int nv = limit - kKeys * j;
+      if (p.page_table && ms.flags[(tiles + j) % kFlagRing]) nv = 0;  // a bad page
+      if (__any_sync(0xffffffffu, nv < kKeys)) {
+        // few key tiles: masked in place, so that the others pay only the branch
+#pragma unroll 1
+        for (int c = 0; c < kKeys; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(ts + c, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) r[k] = c + k < nv ? r[k] : 0xff800000u;  // -inf
+          tmem_st32(ts + c, r);
+        }
+        tmem_wait_st();
+      }
       float x[kKeys];
       {
         uint32_t r[2][32];
@@ -450,17 +467,6 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
         tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < kKeys; ++k) x[k] = __uint_as_float(r[k >> 5][k & 31]);
-      }
-      if (p.negate) {
-#pragma unroll
-        for (int k = 0; k < kKeys; ++k) x[k] = -x[k];
-      }
-      int nv = limit - kKeys * j;
-      if (p.page_table && ms.flags[(tiles + j) % kFlagRing]) nv = 0;  // a bad page
-      const bool masked = __any_sync(0xffffffffu, nv < kKeys);
-      if (masked) {
-#pragma unroll
-        for (int k = 0; k < kKeys; ++k) x[k] = k < nv ? x[k] : -INFINITY;
       }
       float mxs[4];
 #pragma unroll
