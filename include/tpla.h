@@ -485,7 +485,7 @@ TPLA_API int tpla_kv_decode(const tpla_tensor* q, const tpla_tensor* k_cache,
  *   out    [T, Hq, Dv], F32 or q's type, rows on 16-byte boundaries; lse
  *          [T, Hq, 1] f32 or NULL; scale, workspace as in tpla_kv_decode.
  * Keys and values of a request must be finite (a later token's infinity or
- * NaN in v reaches earlier rows of its 128-key tile through a weight of 0);
+ * NaN in v reaches earlier rows of its 64-key tile through a weight of 0);
  * what stands behind its last key is never used.
  * Limits (TPLA_ERR_UNSUPPORTED): B <= 2^20, T and Tk <= 2^30, Hq <= 4096.
  */

@@ -193,7 +193,8 @@ int check_results(const tpla_tensor* out, const tpla_tensor* lse, int dtype, int
       out->shape[1] != Hq || out->shape[2] != Dv)
     return TPLA_ERR_INVALID_ARG;
   if (lse && (!check_tensor(lse, TPLA_F32, 3) || lse->shape[0] != rows || lse->shape[1] != Hq ||
-              lse->shape[2] != 1))
+              lse->shape[2] != 1 || (rows > 1 && lse->stride[0] == 0) ||
+              (Hq > 1 && lse->stride[1] == 0)))
     return TPLA_ERR_INVALID_ARG;
   return TPLA_OK;
 }

@@ -104,11 +104,12 @@ bool expect(Py_ssize_t have, Py_ssize_t want) {
   return false;
 }
 
-// The caller's workspace where it is large enough, else a new one.
+// The caller's workspace where it is one run of memory and large enough, else
+// a new one.
 void* workspace(Arg* ws, size_t need, const at::Tensor& like, size_t* bytes) {
   *bytes = 0;
   if (need == 0) return nullptr;
-  if (ws->t.defined()) *bytes = (size_t)ws->t.numel() * ws->t.element_size();
+  if (ws->t.defined() && ws->t.is_contiguous()) *bytes = (size_t)ws->t.numel() * ws->t.element_size();
   if (*bytes < need) {
     ws->t = at::empty({(int64_t)need}, like.options().dtype(at::kByte).requires_grad(false));
     *bytes = need;

@@ -16,8 +16,9 @@
 //    two S buffers of 64 columns there: while the softmax works on one S the
 //    tensor core fills the other, so neither waits out the other's latency.
 //    Three threads issue the products (Q K^T of A, of B, and both P V), so
-//    that the waits of one pass while the others feed the tensor core.  P goes over its own S as 16-bit pairs, the A
-//    operand from TMEM: 2 x (128 + Dv) of the 512 columns in all.  (With one S
+//    that the waits of one pass while the others feed the tensor core.  P goes
+//    over its own S as 16-bit pairs, the A operand from TMEM: 2 x (128 + Dv)
+//    of the 512 columns in all.  (With one S
 //    of 128 keys, Q K^T had to wait for P V, P V for the softmax and the
 //    softmax for Q K^T: 4450 cycles for 128 keys of both tiles against 2048 of
 //    tensor work.  N = 64 costs 48 cycles where N = 128 costs 64, because Q
