@@ -438,7 +438,11 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
     const int held = it.e.kvlen - kKeys * it.e.j0;  // keys from this piece's first on
     const int limit = (live ? limit_of(p, it.e, tok) : it.e.kvlen) - kKeys * it.e.j0;
     const int n = t ? it.n[1] : it.n[0];
-    float m = -INFINITY, l = 0.f, lx = 0.f;  // maximum; sums of the 16-bit and the f32 weights
+    // The maximum, and the f32 sum of the weights before their rounding to 16
+    // bits for P V: only the numerator carries that rounding (half a step a
+    // weight).  Summing the rounded weights too, as the divisor, took 3-4 % of
+    // the time and gained 2 % of the error (mean relative 2.10e-3 / 2.14e-3).
+    float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j, ++cnt) {
       const int buf = cnt & 1;
       const uint32_t ts = tS + kKeys * buf;
@@ -486,7 +490,6 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
         const float factor = resc ? ex2(m - mx) : 1.f;
         if (resc) m = mx;
         l *= factor;
-        lx *= factor;
 #pragma unroll
         for (int c = 0; c < DV; c += 32) {
           uint32_t o[32];
@@ -515,7 +518,7 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
       }
       const float mu = m == -INFINITY ? 0.f : m;
       const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
-      uint64_t s16 = f2_pack(0.f, 0.f), s32 = f2_pack(0.f, 0.f);
+      uint64_t sum = f2_pack(0.f, 0.f);
       uint32_t pk[32];
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
@@ -524,16 +527,12 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
         e0 = ex2(e0);
         e1 = ex2(e1);
         pk[k] = T::pack(e0, e1);
-        const float2 e = T::unpack(pk[k]);
-        s32 = f2_add(s32, f2_pack(e0, e1));
-        s16 = f2_add(s16, f2_pack(e.x, e.y));
+        sum = f2_add(sum, f2_pack(e0, e1));
       }
       tmem_st32(ts, pk);  // over this row's own scores: they are in registers
       float a, b;
-      f2_unpack(s16, a, b);
+      f2_unpack(sum, a, b);
       l += a + b;
-      f2_unpack(s32, a, b);
-      lx += a + b;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -604,7 +603,7 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
       }
     }
     if (live && (p.lse || it.slot >= 0)) {
-      const float lse = lx > 0.f ? (m + log2f(lx)) * kLn2 : (lx == 0.f ? -INFINITY : NAN);
+      const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : NAN);
       if (it.slot >= 0)
         p.part_l[prow] = lse;
       else
