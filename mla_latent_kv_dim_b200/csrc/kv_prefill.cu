@@ -63,6 +63,12 @@ constexpr int kBuckets = 2048;  // of the items' lengths
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
+// One pair of weights in this many comes from the FMA pipe instead of the
+// exponential unit, which both warpgroups wait for at the same time.  None, one
+// in 8, 4, 3: chunk of four prompts 200, 194, 184, 185 us; packed 91, 87, 84, 85.
+// Not where Dk is 192: there Q K^T takes longer than the exponentials (128
+// heads of 4096 tokens 695 us without, 708 with).
+constexpr int kFmaEvery = 4;
 constexpr int kMinPiece = 8;  // key tiles; a shorter piece is mostly fixed work
 
 struct Entry {  // two query tiles of one request
@@ -523,9 +529,14 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
         float e0, e1;
-        f2_unpack(f2_fma(f2_pack(x[2 * k], x[2 * k + 1]), sc, nm), e0, e1);
-        e0 = ex2(e0);
-        e1 = ex2(e1);
+        const uint64_t y = f2_fma(f2_pack(x[2 * k], x[2 * k + 1]), sc, nm);
+        if (DK < 192 && k % kFmaEvery == kFmaEvery / 2) {
+          f2_ex2_fma(y, e0, e1);
+        } else {
+          f2_unpack(y, e0, e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+        }
         pk[k] = T::pack(e0, e1);
         sum = f2_add(sum, f2_pack(e0, e1));
       }

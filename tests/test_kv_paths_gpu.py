@@ -189,3 +189,49 @@ def test_library_managed_workspaces(cuda_dev):
     a2, _ = tp.kv_decode(q[:2], kc, vc, n, pt, scale, workspace=sparse)
     assert tp.launch_count() == before + 2 and torch.equal(a, a2)
     assert tp.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_weights_of_either_exponential(cuda_dev, dtype):
+    """A row whose sum is one key of score 0 and 16 r keys of score s, these in
+    every column of a key tile in turn: its log-sum-exp is
+    ln(1 + 16 r e^s).  Of the weights' relative error (2.2e-7, 2 ulp of the
+    exponential unit being 2.4e-7) and that of s / ln 2 in f32, |s| 2^-23 (two
+    roundings), the logarithm keeps at most the same absolute error; its own
+    rounding is a few 2^-24 of 1 + |lse|."""
+    r, D = 40, 64
+    scores = [-0.25 * i for i in range(60)] + [0.0, -40.0, -80.0]
+    far = -256.0  # e^-256 is 0 beside any of them
+    q = torch.zeros((1, 1, D), dtype=dtype)
+    q[..., 0] = 1
+    for column in range(8):
+        rows = []
+        for s in scores:
+            k = torch.full((64 * (r + 1),), far)
+            k[0] = 0
+            k[64:].view(-1, 64)[:, [column + 8 * i for i in range(8)]] = s
+            k[64:].view(-1, 64)[:, [(column + 1) % 8 + 8 * i for i in range(8)]] = s
+            rows.append(k)
+        B, L = len(scores), 64 * (r + 1)
+        k = torch.zeros((B * L, 1, D), dtype=dtype)
+        k[:, 0, 0] = torch.cat(rows).to(dtype)
+        v = torch.ones((B * L, 1, D), dtype=dtype)
+        out, lse = tp.kv_prefill(q.expand(B, 1, D).contiguous().to(cuda_dev), k.to(cuda_dev),
+                                 v.to(cuda_dev), _rows([1] * B).to(cuda_dev),
+                                 _rows([L] * B).to(cuda_dev), scale=1.0)
+        s = torch.tensor(scores, dtype=torch.float64)
+        want = torch.log1p(16 * r * s.exp())
+        err = (lse[:, 0, 0].double().cpu() - want).abs()
+        tol = 2.4e-7 + s.abs() * 2.0 ** -23 + (1 + want) * 2.0 ** -22
+        assert (err <= tol).all(), (column, (err / tol).max())
+        # values of 1: what the rounding of the weights leaves of the sum
+        half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -11
+        share = 1 - torch.exp(-want)  # what the rounded weights have of the sum
+        # (half a step each, in fp16 below 2^-14 the absolute 2^-25), and less
+        # than a unit in the last place, 2^-23 of a sum near 1, that each of the
+        # 4 (r + 1) matrix products of 16 keys drops as it adds into f32
+        tol = half * share + 4 * (r + 1) * 2.0 ** -23 + 1e-6
+        if dtype == torch.float16:
+            tol = tol + 16 * r * 2.0 ** -25
+        assert ((out.double().cpu()[:, 0] - 1).abs() <= tol[:, None]).all()
+    assert tp.device_status() == 0
