@@ -69,6 +69,7 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // Not where Dk is 192: there Q K^T takes longer than the exponentials (128
 // heads of 4096 tokens 695 us without, 708 with).
 constexpr int kFmaEvery = 4;
+constexpr int64_t kL2Share = 96 << 20;  // bytes of keys and values that the L2 keeps
 constexpr int kMinPiece = 8;  // key tiles; a shorter piece is mostly fixed work
 
 struct Entry {  // two query tiles of one request
@@ -92,6 +93,7 @@ struct Params {
   int num_blocks;
   int cap_rows;
   int B, T, Hkv, g, gg, groups, tpt;  // gg heads of a row group, tpt tokens of a tile
+  int paired;            // the order of the items, see Items
   int causal;
   float scale_log2;      // |softmax scale| * log2(e) (> 0; see the launcher)
   int negate;            // scale < 0
@@ -164,7 +166,9 @@ __device__ __forceinline__ int item_count(const Params& p) {
 
 // A block's items: every gridDim.x-th of the list, in alternating direction
 // so that the blocks with the longest of one round get the shortest of the
-// next.
+// next.  Or (`paired`: one prompt) head after head, a long item and the short
+// one that makes up for it together, so that every pair is the same work and
+// few heads' keys and values are in use at a time.
 struct Items {
   int total, heads, round;
   __device__ explicit Items(const Params& p)
@@ -173,18 +177,35 @@ struct Items {
   // the next item with keys, or (want_empty) the next of any kind
   __device__ bool next(const Params& p, Item& it, bool want_empty = false) {
     for (;;) {
-      const int c = round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
-      const long long idx = (long long)round * gridDim.x + c;
-      if ((long long)round * gridDim.x >= total) return false;
-      ++round;
-      if (idx >= total) continue;
-      get(p, (int)idx, it);
+      int x, h;
+      if (p.paired) {
+        const int entries = total / heads, pairs = (entries + 1) / 2;
+        const long long at = (long long)(round >> 1) * gridDim.x, pair = at + blockIdx.x;
+        const bool second = round & 1;
+        if (at >= (long long)pairs * heads) return false;
+        ++round;
+        if (pair >= (long long)pairs * heads) continue;
+        h = (int)pair / pairs;
+        x = (int)pair - h * pairs;
+        if (second) {
+          if (x == entries - 1 - x) continue;  // the middle one has no other
+          x = entries - 1 - x;
+        }
+      } else {
+        const int c = round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x;
+        const long long idx = (long long)round * gridDim.x + c;
+        if ((long long)round * gridDim.x >= total) return false;
+        ++round;
+        if (idx >= total) continue;
+        x = (int)idx / heads;
+        h = (int)idx - x * heads;
+      }
+      get(p, x, h, it);
       if (it.nmax > 0 || want_empty) return true;
     }
   }
 
-  __device__ void get(const Params& p, int idx, Item& it) const {
-    const int x = idx / heads, h = idx - x * heads;
+  __device__ void get(const Params& p, int x, int h, Item& it) const {
     it.hk = h / p.groups;
     it.rg = h - it.hk * p.groups;
     if (p.count) {
@@ -880,6 +901,7 @@ struct Shape {
   int slots;        // partial results (times the heads) of items in pieces, 0: none are cut
   int rows_slot;
   int64_t capacity; // entries of the list
+  int paired;
   size_t list_bytes, join_bytes, o_bytes, l_bytes;
 };
 
@@ -902,6 +924,14 @@ Shape shape(const KvPrefillProblem& p, int sms) {
   s.slots = cut ? (4 * sms + s.heads - 1) / s.heads : 0;
   s.rows_slot = (p.T < 2 * s.tpt ? p.T : 2 * s.tpt) * s.gg;
   s.capacity = s.entries + (cut ? 2 * sms : 0);
+  // All heads' longest items first would have every head's keys and values in
+  // use at once.  Where the L2 (126 MB) does not keep those, the items of one
+  // prompt go head after head in pairs; the last round of pairs must be nearly
+  // full, because a pair is up to twice an item.  128 heads of 4096 tokens
+  // (335 MB of keys and values): 728 us longest first, 648 in pairs.
+  const int64_t pairs = ((s.entries - p.B + 1) / 2) * s.heads, rounds = (pairs + sms - 1) / sms;
+  s.paired = !s.planned && pairs > 0 && rounds * sms <= pairs + pairs / 16 &&
+             p.kv.cap_rows * (p.kv.Dk + p.kv.Dv) * 2 * p.kv.Hkv > kL2Share;
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   s.list_bytes = up((size_t)s.capacity * sizeof(Entry));
   s.join_bytes = up((size_t)s.slots * sizeof(Join));
@@ -1024,6 +1054,7 @@ cudaError_t launch_kv_prefill(const KvPrefillProblem& dp, void* ws, cudaStream_t
   p.out32 = dp.out_dtype != TPLA_F32 && (reinterpret_cast<uintptr_t>(dp.out) & 31) == 0 &&
             (dp.T == 1 || dp.o_st % 16 == 0) && (dp.Hq == 1 || dp.o_sh % 16 == 0);
   p.rows_slot = s.rows_slot;
+  p.paired = s.paired;
   const int64_t items = s.capacity * s.heads;
   if (items > (1LL << 31) - 1 - s.sms) return cudaErrorInvalidValue;
   if (s.planned) {

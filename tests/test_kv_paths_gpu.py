@@ -235,3 +235,26 @@ def test_weights_of_either_exponential(cuda_dev, dtype):
             tol = tol + 16 * r * 2.0 ** -25
         assert ((out.double().cpu()[:, 0] - 1).abs() <= tol[:, None]).all()
     assert tp.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [2700, 2900])
+def test_one_prompt_of_many_heads(cuda_dev, T):
+    """Keys and values beyond the L2: heads one after another, tiles in pairs
+    (an odd and an even number of them).  Some rows of some heads against 64
+    bits, and every row of every head against the same call for those heads
+    alone, bit by bit."""
+    gen = torch.Generator(device=cuda_dev).manual_seed(6)
+    H, D, scale = 148, 64, 0.125
+    q, k, v = (torch.randn((T, H, D), generator=gen, device=cuda_dev).bfloat16() for _ in range(3))
+    cu = _rows([T]).to(cuda_dev)
+    out, lse = tp.kv_prefill(q, k, v, cu, scale=scale)
+    rows, heads = list(range(0, T, 97)) + [T - 1], [0, 1, 73, 146, 147]
+    ref = attend64(q[rows][:, heads].cpu(), k[:, heads].cpu(), v[:, heads].cpu(), scale,
+                   [r + 1 for r in rows])
+    check_attention(out[rows][:, heads], lse[rows][:, heads], ref, torch.bfloat16, torch.float32,
+                    "sample")
+    for h in range(0, H, 37):
+        part = slice(h, h + 37)
+        a, b = tp.kv_prefill(q[:, part], k[:, part], v[:, part], cu, scale=scale)
+        assert torch.equal(a, out[:, part]) and torch.equal(b, lse[:, part])
+    assert tp.device_status() == 0
