@@ -21,6 +21,13 @@
 // warp, and they meet once at the end of a (request, head) segment.  Up to 16
 // rows the consumers are two groups of four warps, each with its slice, its
 // ring and its producer: one group's segment end passes while the other reads.
+//
+// Measured (B200, bytes of the cache against a copy's 6542 GB/s): 4 requests of
+// 131072 tokens, 64 heads over 8 of 128: 317 us, 6.8 TB/s, 104 %; 32 of 2048 to
+// 4096, 32 over 8: 74 us, 86 %; 13 ragged ones of 16 heads, 192 / 128, f16: 70
+// us, 79 % (the slices' ends: start, last page, joins, merge); 1 of 256 tokens:
+// 8.6 us, nearly all fixed (start 2, one page 2.5, join 0.7, merge launch and
+// read 1.5).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

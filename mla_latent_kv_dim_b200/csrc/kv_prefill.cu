@@ -18,11 +18,11 @@
 //    Three threads issue the products (Q K^T of A, of B, and both P V), so
 //    that the waits of one pass while the others feed the tensor core.  P goes
 //    over its own S as 16-bit pairs, the A operand from TMEM: 2 x (128 + Dv)
-//    of the 512 columns in all.  (With one S
-//    of 128 keys, Q K^T had to wait for P V, P V for the softmax and the
-//    softmax for Q K^T: 4450 cycles for 128 keys of both tiles against 2048 of
-//    tensor work.  N = 64 costs 48 cycles where N = 128 costs 64, because Q
-//    is read again.)
+//    of the 512 columns in all.  (With one S of 128 keys a tile Q K^T waits for
+//    P V, P V for the softmax and the softmax for Q K^T: 4450 cycles for 128
+//    keys of both tiles against 2048 of tensor work.  In exchange N = 64 takes
+//    48 cycles where N = 128 takes 64, because Q is read again: 1152 cycles for
+//    64 keys of both tiles at 128 columns);
 //  * a thread owns a row: no exchange for the row maximum.  O is rescaled
 //    only when the maximum has grown by more than 2^8;
 //  * K and V tiles go through a ring of key tiles (64-column chunks of 64 rows,
@@ -32,6 +32,19 @@
 //    too few items for the GPU (a short chunk after a long prefix), that
 //    kernel cuts their keys into pieces, whose normalised results a third
 //    kernel joins by their log-sum-exp.
+//
+// Measured (B200 at 1.97 GHz, bf16 in and out; of the burst rate of a library
+// product, 1651 TFLOP/s): 16384 tokens of 8 heads over one of 128: 451 us, 1218
+// TFLOP/s, 74 %; 128 heads of 4096 tokens, 192 / 128 wide: 648 us, 64 %; chunks
+// of four prompts after 4000 to 8000 tokens (f16, paged): 186 us, 54 %; twelve
+// prompts of 33 to 1500 tokens: 86 us, 39 %; one of 77 tokens: 7.6 us, mostly
+// fixed (an empty kernel takes 1 us, the start 2, a chain of two key tiles 3).
+// What bounds it is feeding the tensor core: of 1750 cycles a step of 64 keys at
+// Dk = 128 its pipe is taken 82 % of the time (1430 cycles, 1024 of them at the
+// full rate), the exponential unit 44 %, the schedulers 53 %; beyond that the two
+// warpgroups reach the exponentials at the same time.  (Two warpgroups a query
+// tile, 16 softmax warps of 104 registers, in three forms: 8 to 25 % slower.)
+// The short calls end in blocks with nothing left to do.
 #include <cuda_runtime.h>
 
 #include <mutex>
