@@ -36,7 +36,7 @@
 // Measured (B200 at 1.97 GHz, bf16 in and out; of the burst rate of a library
 // product, 1651 TFLOP/s): 16384 tokens of 8 heads over one of 128: 451 us, 1218
 // TFLOP/s, 74 %; 128 heads of 4096 tokens, 192 / 128 wide: 648 us, 64 %; chunks
-// of four prompts after 4000 to 8000 tokens (f16, paged): 186 us, 54 %; twelve
+// of four prompts after 4000 to 8000 tokens (f16, paged): 177 us, 57 %; twelve
 // prompts of 33 to 1500 tokens: 86 us, 39 %; one of 77 tokens: 7.6 us, mostly
 // fixed (an empty kernel takes 1 us, the start 2, a chain of two key tiles 3).
 // What bounds it is feeding the tensor core: of 1750 cycles a step of 64 keys at
@@ -842,61 +842,70 @@ __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, E
 
 // Joins the pieces of an item,
 //   lse = ln sum_i exp(lse_i),  out = sum_i exp(lse_i - lse) out_i:
-// a thread per row and 8 columns, the rows of a warp side by side.
-constexpr int kJoinThreads = 128;
+// a thread per row and 16 columns, the rows of a warp side by side.  (8 columns
+// and a quarter of the blocks: chunk of four prompts 187 us, now 179.)
+constexpr int kJoinThreads = 128, kJoinColumns = 16;
 
 template <int DV>
 __global__ void __launch_bounds__(kJoinThreads) kv_prefill_join_kernel(const Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int heads = p.Hkv * p.groups, n = p.count[1];
-  constexpr int kC = DV / 8;  // column groups of a row
+  constexpr int kN = kJoinColumns, kC = DV / kN;  // kC threads to a row
   const int rows = p.rows_slot;
   for (int x = blockIdx.x; x < n * heads; x += gridDim.x) {
     const Join jn = p.joins[x / heads];
     const int h = x % heads, hk = h / p.groups, rg = h - hk * p.groups;
     for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < rows * kC;
          e += gridDim.y * kJoinThreads) {
-      const int c = e / rows, row = e - c * rows;
+      const int c = e / rows, row = e - c * rows;  // the rows of a warp lie side by side
       const int tok = jn.t0 + row / p.gg, head = rg * p.gg + row % p.gg;
       if (tok >= jn.qlen || head >= p.g) continue;
       const float* l = p.part_l + ((int64_t)jn.slot * heads + h) * rows + row;
       const float4* o = reinterpret_cast<const float4*>(p.part_o) +
-                        (((int64_t)jn.slot * heads + h) * (DV / 4) + 2 * c) * rows + row;
+                        (((int64_t)jn.slot * heads + h) * (DV / 4) + kN / 4 * c) * rows + row;
       const int64_t step = (int64_t)heads * rows;  // between two pieces
       float top = -INFINITY;
       for (int i = 0; i < jn.pieces; ++i) top = fmaxf(top, l[i * step]);
       const float ref = top == -INFINITY ? 0.f : top;
-      float sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      float sum = 0.f, acc[kN];
+#pragma unroll
+      for (int k = 0; k < kN; ++k) acc[k] = 0.f;
+#pragma unroll 2
       for (int i = 0; i < jn.pieces; ++i) {
         const float w = expf(l[i * step] - ref);
-        const float4 a = o[i * step * (DV / 4)], b = o[i * step * (DV / 4) + rows];
         sum += w;
-        acc[0] = fmaf(w, a.x, acc[0]);
-        acc[1] = fmaf(w, a.y, acc[1]);
-        acc[2] = fmaf(w, a.z, acc[2]);
-        acc[3] = fmaf(w, a.w, acc[3]);
-        acc[4] = fmaf(w, b.x, acc[4]);
-        acc[5] = fmaf(w, b.y, acc[5]);
-        acc[6] = fmaf(w, b.z, acc[6]);
-        acc[7] = fmaf(w, b.w, acc[7]);
+#pragma unroll
+        for (int k = 0; k < kN; k += 4) {
+          const float4 a = o[i * step * (DV / 4) + k / 4 * rows];
+          acc[k] = fmaf(w, a.x, acc[k]);
+          acc[k + 1] = fmaf(w, a.y, acc[k + 1]);
+          acc[k + 2] = fmaf(w, a.z, acc[k + 2]);
+          acc[k + 3] = fmaf(w, a.w, acc[k + 3]);
+        }
       }
       const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : NAN);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] *= inv;
+      for (int k = 0; k < kN; ++k) acc[k] *= inv;
       const int64_t off = (int64_t)(jn.q0 + tok) * p.o_st + (int64_t)(hk * p.g + head) * p.o_sh +
-                          8 * c;
+                          kN * c;
       if (p.out_dtype == TPLA_F32) {
         float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + off);
-        d[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        d[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-      } else {
-        uint32_t v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kN; k += 4)
+          d[k / 4] = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+      } else {
+        uint32_t v[kN / 2];
+#pragma unroll
+        for (int k = 0; k < kN / 2; ++k)
           v[k] = p.out_dtype == TPLA_F16 ? F16::pack(acc[2 * k], acc[2 * k + 1])
                                          : Bf16::pack(acc[2 * k], acc[2 * k + 1]);
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + off) =
-            make_uint4(v[0], v[1], v[2], v[3]);
+        uint16_t* const d = reinterpret_cast<uint16_t*>(p.out) + off;
+        if (p.out32) {
+          st_global_v8(d, v);
+        } else {
+          *reinterpret_cast<uint4*>(d) = make_uint4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<uint4*>(d + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+        }
       }
       if (p.lse && c == 0)
         p.lse[(int64_t)(jn.q0 + tok) * p.l_st + (int64_t)(hk * p.g + head) * p.l_sh] =
@@ -966,7 +975,7 @@ int sm_count(int device) {
 
 template <typename T, int DK, int DV>
 cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
-                   const Params& p, int grid, int dev, cudaStream_t stream) {
+                   const Params& p, int slots, int grid, int dev, cudaStream_t stream) {
   using C = Cfg<T, DK, DV>;
   static std::mutex mu;
   static uint64_t ready = 0;  // devices whose shared-memory limit is raised
@@ -992,7 +1001,10 @@ cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorM
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_prefill_kernel<T, DK, DV>, qm, km, vm, p);
   count_launch();
   if (e != cudaSuccess || !p.part_o) return e;
-  cfg.gridDim = dim3(64, 8);
+  // an item has two pieces or more; two runs of columns a thread
+  const int runs = p.rows_slot * (DV / kJoinColumns);
+  cfg.gridDim = dim3((unsigned)((slots * p.Hkv * p.groups + 1) / 2),
+                     (unsigned)((runs + 2 * kJoinThreads - 1) / (2 * kJoinThreads)));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, kv_prefill_join_kernel<DV>, p);
@@ -1002,10 +1014,11 @@ cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorM
 
 template <typename T>
 cudaError_t launch_type(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
-                        const Params& p, int dk, int dv, int grid, int dev, cudaStream_t stream) {
-  if (dk == 64 && dv == 64) return launch<T, 64, 64>(qm, km, vm, p, grid, dev, stream);
-  if (dk == 128 && dv == 128) return launch<T, 128, 128>(qm, km, vm, p, grid, dev, stream);
-  if (dk == 192 && dv == 128) return launch<T, 192, 128>(qm, km, vm, p, grid, dev, stream);
+                        const Params& p, int dk, int dv, int slots, int grid, int dev,
+                        cudaStream_t stream) {
+  if (dk == 64 && dv == 64) return launch<T, 64, 64>(qm, km, vm, p, slots, grid, dev, stream);
+  if (dk == 128 && dv == 128) return launch<T, 128, 128>(qm, km, vm, p, slots, grid, dev, stream);
+  if (dk == 192 && dv == 128) return launch<T, 192, 128>(qm, km, vm, p, slots, grid, dev, stream);
   return cudaErrorInvalidValue;
 }
 
@@ -1090,8 +1103,8 @@ cudaError_t launch_kv_prefill(const KvPrefillProblem& dp, void* ws, cudaStream_t
     }
   }
   const int grid = (int)(items < s.sms ? items : s.sms);
-  return kv.f16 ? launch_type<F16>(qm, km, vm, p, kv.Dk, kv.Dv, grid, dev, stream)
-                : launch_type<Bf16>(qm, km, vm, p, kv.Dk, kv.Dv, grid, dev, stream);
+  return kv.f16 ? launch_type<F16>(qm, km, vm, p, kv.Dk, kv.Dv, s.slots, grid, dev, stream)
+                : launch_type<Bf16>(qm, km, vm, p, kv.Dk, kv.Dv, s.slots, grid, dev, stream);
 }
 
 cudaError_t status_read_clear_kv_prefill(int* code) {
