@@ -258,3 +258,32 @@ def test_one_prompt_of_many_heads(cuda_dev, T):
         a, b = tp.kv_prefill(q[:, part], k[:, part], v[:, part], cu, scale=scale)
         assert torch.equal(a, out[:, part]) and torch.equal(b, lse[:, part])
     assert tp.device_status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_that_is_no_number(cuda_dev, bad):
+    """Its own rows are NaN, every other row keeps its bits: in a prompt, in a
+    prompt cut along its keys, and in a decode step split over the GPU."""
+    gen = torch.Generator().manual_seed(8)
+    lens, Hq, Hkv, D, scale = [5000, 300], 8, 2, 128, 0.09
+    kc, pt = paged_cache(lens, Hkv, D, torch.bfloat16, gen)
+    vc = torch.randn(kc.shape, generator=gen).bfloat16()
+    kc, vc, pt = kc.to(cuda_dev), vc.to(cuda_dev), pt.to(cuda_dev)
+    q = torch.randn((90, Hq, D), generator=gen).bfloat16().to(cuda_dev)
+    worse = q.clone()
+    worse[0, 3, 5] = worse[77, 0, 100] = bad
+    n = torch.tensor(lens, dtype=torch.int32, device=cuda_dev)
+    cu = _rows([60, 30]).to(cuda_dev)
+    for call in (lambda x: tp.kv_prefill(x, kc, vc, cu, seq_lens=n, page_table=pt, scale=scale),
+                 lambda x: tp.kv_prefill(x[:30], kc[0], vc[0], _rows([30]).to(cuda_dev),
+                                         _rows([64]).to(cuda_dev), scale=scale),
+                 lambda x: tp.kv_decode(x[:2], kc, vc, n, pt, scale)):
+        want, want_lse = call(q)
+        out, lse = call(worse)
+        hit = torch.zeros(out.shape[:2], dtype=torch.bool, device=cuda_dev)
+        hit[0, 3] = True
+        if out.shape[0] > 77:
+            hit[77, 0] = True
+        assert out[hit].isnan().all() and lse[hit].isnan().all()
+        assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+    assert tp.device_status() == 0
