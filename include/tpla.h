@@ -480,8 +480,12 @@ TPLA_API int tpla_kv_decode(const tpla_tensor* q, const tpla_tensor* k_cache,
  *          paged: the caches, with page_table and seq_lens [B] int32 (L_b:
  *          cached tokens and the prompt's own, stored before this call, for
  *          instance by tpla_kv_append); cu_k NULL.
- *   cu_q, cu_k  [B + 1] int32, contiguous, rising; entries outside the
- *          tensors are clipped and recorded as TPLA_ERR_DEVICE_BOUNDS.
+ *   cu_q, cu_k  [B + 1] int32, contiguous, rising.  Entries outside the
+ *          tensors are clipped; a request whose end lies before its start has
+ *          no rows (no keys).  Both are recorded as TPLA_ERR_DEVICE_BOUNDS.
+ *          Where offsets fall and rise again, a row of two requests gets
+ *          values of either; where requests claim so many rows that their
+ *          tiles would outgrow the workspace, the call writes nothing.
  *   out    [T, Hq, Dv], F32 or q's type, rows on 16-byte boundaries; lse
  *          [T, Hq, 1] f32 or NULL; scale, workspace as in tpla_kv_decode.
  * Keys and values of a request must be finite (a later token's infinity or

@@ -725,35 +725,56 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant_
 // item's last token.  One block; a warp takes a request at a time.  The order
 // within a bucket is not fixed, and no result depends on it.
 //
-// With `slots` > 0 items may be cut: the work of a call with few items is
-// meant to fill `fill` blocks twice, so no piece is longer than that share.
+// With `cut` items may be cut: the work of a call with few items is meant to
+// fill `fill` blocks twice, so no piece is longer than that share.
+//
+// Offsets that rise give at most `room` items, T / tb + B.  Offsets that fall
+// can claim rows again and again; where they claim more items than that, the
+// call is answered with no row at all, before anything is counted in 32 bits.
+// With at most `room` items the list has an entry, and the pieces a slot, for
+// all: with W key tiles in all items, a piece may be W heads / (2 fill) long or
+// longer, so the pieces are at most W / longest <= 2 fill / heads and one an
+// item; an item that is cut is longer than one piece, so there are at most
+// 2 fill / heads of those and 4 fill / heads pieces of theirs.
 __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, Entry* list,
-                                                               Join* joins, int* count,
-                                                               int capacity, int slots,
-                                                               int fill) {
+                                                               Join* joins, int* count, int room,
+                                                               bool cut, int fill) {
   __shared__ int hist[kBuckets];
   __shared__ int top, warp_sum[32], n_joins, n_slots;
-  __shared__ unsigned long long work;
+  __shared__ unsigned long long claimed, work;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tb = 2 * p.tpt;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = threadIdx.x; i < kBuckets; i += 1024) hist[i] = 0;
   if (threadIdx.x == 0) {
     top = n_joins = n_slots = 0;
-    work = 0;
+    claimed = work = 0;
   }
   __syncthreads();
   auto tiles_of = [&](const Entry& e, int t0) {
     return (limit_of(p, e, min(t0 + tb, e.qlen) - 1) + kKeys - 1) / kKeys;
   };
   int most = 0;
+  unsigned long long items = 0;
   for (int b = threadIdx.x; b < p.B; b += 1024) {
     Entry e;
     request(p, b, e);
     most = max(most, (e.kvlen + kKeys - 1) / kKeys);
+    items += (e.qlen + tb - 1) / tb;
   }
   if (most) atomicMax(&top, most);
-  if (slots > 0) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) items += __shfl_down_sync(0xffffffffu, items, o);
+  if (lane == 0 && items) atomicAdd(&claimed, items);
+  __syncthreads();
+  if (claimed > (unsigned long long)room) {
+    if (threadIdx.x == 0) {
+      bounds();
+      count[0] = count[1] = 0;
+    }
+    return;
+  }
+  if (cut) {
     unsigned long long mine = 0;
     for (int b = warp; b < p.B; b += 32) {
       Entry e;
@@ -769,7 +790,7 @@ __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, E
   const int share = (int)min((unsigned long long)(1 << 30),
                              (work * heads + 2 * fill - 1) / (unsigned long long)(2 * fill));
   const int longest = max(kMinPiece, share);
-  auto pieces_of = [&](int tiles) { return slots > 0 ? max(1, (tiles + longest - 1) / longest) : 1; };
+  auto pieces_of = [&](int tiles) { return cut ? max(1, (tiles + longest - 1) / longest) : 1; };
   auto bucket = [&](int tiles) { return kBuckets - 1 - (tiles >> shift); };  // 0: the longest
   for (int b = warp; b < p.B; b += 32) {
     Entry e;
@@ -794,7 +815,7 @@ __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, E
     for (int i = 0; i < warp; ++i) before += warp_sum[i];
     hist[2 * threadIdx.x] = before;
     hist[2 * threadIdx.x + 1] = before + a;
-    if (threadIdx.x == 1023) count[0] = min(before + a + z, capacity);
+    if (threadIdx.x == 1023) count[0] = before + a + z;
   }
   __syncthreads();
   for (int b = warp; b < p.B; b += 32) {
@@ -803,31 +824,18 @@ __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, E
     e.pad[0] = e.pad[1] = e.pad[2] = 0;
     for (int t0 = lane * tb; t0 < e.qlen; t0 += 32 * tb) {
       const int tiles = tiles_of(e, t0), k = pieces_of(tiles), len = (tiles + k - 1) / k;
+      const int at = atomicAdd(&hist[bucket(len)], k);
       e.t0 = t0;
       e.slot = -1;
-      const int at = atomicAdd(&hist[bucket(len)], k);
-      if (at + k > capacity) {  // requests that overlap in q can ask for more
-        bounds();
-        for (int i = at; i < capacity; ++i) list[i].qlen = list[i].kvlen = list[i].t0 = 0;
-        continue;
-      }
       if (k > 1) {
-        const int slot = atomicAdd(&n_slots, k);
-        if (slot + k <= slots) {
-          const int j = atomicAdd(&n_joins, 1);
-          joins[j] = Join{t0, e.q0, e.qlen, slot, k, {0, 0, 0}};
-          e.slot = slot;
-        }
+        e.slot = atomicAdd(&n_slots, k);
+        joins[atomicAdd(&n_joins, 1)] = Join{t0, e.q0, e.qlen, e.slot, k, {0, 0, 0}};
       }
       for (int i = 0; i < k; ++i) {
-        // without a slot (see above) the first piece is the whole item and
-        // the others are empty
-        const bool whole = e.slot < 0;
         Entry x = e;
-        x.j0 = whole ? 0 : i * len;
-        x.j1 = whole ? 1 << 30 : min(tiles, (i + 1) * len);
-        x.slot = whole ? -1 : e.slot + i;
-        if (whole && i > 0) x.qlen = x.t0 = x.kvlen = 0;
+        x.j0 = i * len;
+        x.j1 = min(tiles, x.j0 + len);
+        x.slot = k > 1 ? e.slot + i : -1;
         const int4* s = reinterpret_cast<const int4*>(&x);
         int4* d = reinterpret_cast<int4*>(list + at + i);
         d[0] = s[0];
@@ -937,9 +945,8 @@ Shape shape(const KvPrefillProblem& p, int sms) {
   s.sms = sms;
   s.entries = (int64_t)p.T / (2 * s.tpt) + p.B;
   // Items are cut where full ones would not go round the GPU twice and the
-  // keys are long enough for two pieces.  Cutting makes no piece longer than
-  // half a block's share of the work: at most 2 sms pieces of that length,
-  // and twice as many in all.
+  // keys are long enough for two pieces.  No piece is longer than half a
+  // block's share of the work, which bounds the pieces: see the plan kernel.
   const bool cut = (int64_t)p.T / (2 * s.tpt) * s.heads < 2 * sms &&
                    p.kv.cap_rows >= 2 * kMinPiece * kKeys;
   s.planned = p.B > 1 || cut;
@@ -1088,8 +1095,8 @@ cudaError_t launch_kv_prefill(const KvPrefillProblem& dp, void* ws, cudaStream_t
     int* count = reinterpret_cast<int*>(at);
     Entry* list = reinterpret_cast<Entry*>(at + 256);
     Join* joins = reinterpret_cast<Join*>(at + 256 + s.list_bytes);
-    kv_prefill_plan_kernel<<<1, 1024, 0, stream>>>(p, list, joins, count, (int)s.capacity,
-                                                   s.slots, s.sms);
+    kv_prefill_plan_kernel<<<1, 1024, 0, stream>>>(p, list, joins, count, (int)s.entries,
+                                                   s.slots > 0, s.sms);
     count_launch();
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
