@@ -85,7 +85,7 @@ constexpr int kFmaEvery = 4;
 constexpr int64_t kL2Share = 96 << 20;  // bytes of keys and values that the L2 keeps
 constexpr int kMinPiece = 8;  // key tiles; a shorter piece is mostly fixed work
 
-struct Entry {  // two query tiles of one request
+struct alignas(16) Entry {  // two query tiles of one request; moved as three int4
   int t0;       // first token within the request
   int q0, qlen; // the request's rows of q
   int k0;       // packed: its first row of k
@@ -95,6 +95,7 @@ struct Entry {  // two query tiles of one request
   int slot;     // of its partial result (times the heads), -1: the whole item
   int pad[3];
 };
+static_assert(sizeof(Entry) == 48 && alignof(Entry) == 16, "three int4");
 
 struct Join {  // an item in pieces
   int t0, q0, qlen, slot, pieces, pad[3];
