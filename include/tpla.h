@@ -452,8 +452,9 @@ TPLA_API int tpla_kv_append(const tpla_tensor* k_new, const tpla_tensor* v_new,
  * The cache is read once, split evenly over the GPU's SMs whatever the
  * lengths, and the pieces are joined by the log-sum-exp rule.  What stands
  * behind a request's last token in its page is never used (it may be NaN).
- * Weights are rounded to the 16-bit type for the product with v; sums and
- * the log-sum-exp are f32.
+ * Weights are rounded to the 16-bit type for the product with v (F16: below
+ * 2^-40 of the largest they count as 0), which is divided by the sum of the
+ * rounded weights; sums and the log-sum-exp are f32.
  * Limits (TPLA_ERR_UNSUPPORTED): other widths, B <= 2^20, Hq <= 4096,
  * B * Hq <= 2^30, tokens of a request <= 2^30, pages other than 64 tokens, no
  * sm_100 GPU.
@@ -491,6 +492,9 @@ TPLA_API int tpla_kv_decode(const tpla_tensor* q, const tpla_tensor* k_cache,
  * Keys and values of a request must be finite (a later token's infinity or
  * NaN in v reaches earlier rows of its 64-key tile through a weight of 0);
  * what stands behind its last key is never used.
+ * Weights are rounded to the 16-bit type for the product with v (F16: below
+ * 2^-34 of the largest they count as 0), which is divided by the f32 sum of
+ * the weights before that rounding; the log-sum-exp is of that sum.
  * Limits (TPLA_ERR_UNSUPPORTED): B <= 2^20, T and Tk <= 2^30, Hq <= 4096.
  */
 TPLA_API int tpla_kv_prefill_workspace_size(const tpla_tensor* q, const tpla_tensor* k,

@@ -402,6 +402,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float m[2] = {-INFINITY, -INFINITY};  // running maximum of the scaled scores, log2 units
+    // both lifted by T::kLift
     float lr[2] = {0.f, 0.f};             // sum of the 16-bit weights: normalises the output
     float le[2] = {0.f, 0.f};             // sum of the f32 weights: the log-sum-exp
 
@@ -464,7 +465,8 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             o[i][3] *= f[1];
           }
         }
-        const float ms0 = m[0] == -INFINITY ? 0.f : m[0], ms1 = m[1] == -INFINITY ? 0.f : m[1];
+        const float ms0 = m[0] == -INFINITY ? 0.f : m[0] - T::kLift;
+        const float ms1 = m[1] == -INFINITY ? 0.f : m[1] - T::kLift;
 #pragma unroll
         for (int k = 0; k < C::kNT / 16; ++k) {
           uint32_t a[4];
@@ -538,7 +540,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       f[j] = m[j] == -INFINITY ? 0.f : ex2(m[j] - top) * inv;
       const int rw = rb * 16 + ri;
       if (slice == 0 && (lane & 3) == 0 && rw < nrows) {
-        const float l = sle > 0.f ? (top + log2f(sle)) * kLn2 : (sle == 0.f ? -INFINITY : NAN);
+        const float l = sle > 0.f ? (top + (log2f(sle) - T::kLift)) * kLn2 : (sle == 0.f ? -INFINITY : NAN);
         if (!s.complete)
           p.part_l[(int64_t)s.slot * p.rows + rw] = l;
         else if (p.lse)

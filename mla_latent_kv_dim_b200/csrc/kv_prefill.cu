@@ -24,7 +24,7 @@
 //    48 cycles where N = 128 takes 64, because Q is read again: 1152 cycles for
 //    64 keys of both tiles at 128 columns);
 //  * a thread owns a row: no exchange for the row maximum.  O is rescaled
-//    only when the maximum has grown by more than 2^8;
+//    only when the maximum has grown by more than 2^8 (fp16: 2^6);
 //  * K and V tiles go through a ring of key tiles (64-column chunks of 64 rows,
 //    128-byte swizzle, K-major for Q K^T and MN-major for P V);
 //  * items are handed out longest first (a small kernel sorts them; one
@@ -74,7 +74,6 @@ constexpr int kSmemBytes = 232448;
 constexpr int kMiscBytes = 2048;
 constexpr int kBuckets = 2048;  // of the items' lengths
 constexpr uint32_t kColS = 0, kColO = 256;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 // One pair of weights in this many comes from the FMA pipe instead of the
 // exponential unit, which both warpgroups wait for at the same time.  None, one
@@ -522,7 +521,7 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
         for (int k = 8 + 2 * i; k < kKeys; k += 8) mxs[i] = max3(mxs[i], x[k], x[k + 1]);
       }
       const float mx = fmaxf(max3(mxs[0], mxs[1], mxs[2]), mxs[3]) * p.scale_log2;
-      const bool resc = mx > m + kRescaleThreshold && m != -INFINITY;
+      const bool resc = mx > m + T::kLag && m != -INFINITY;
       if (m == -INFINITY) m = mx;
       if (__any_sync(0xffffffffu, resc)) {
         // O as the P V before this one leaves it (no maximum before the first)
@@ -557,7 +556,7 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
         }
         fence_async_smem();
       }
-      const float mu = m == -INFINITY ? 0.f : m;
+      const float mu = m == -INFINITY ? 0.f : m - T::kLiftLag;
       const uint64_t sc = f2_pack(p.scale_log2, p.scale_log2), nm = f2_pack(-mu, -mu);
       uint64_t sum = f2_pack(0.f, 0.f);
       uint32_t pk[32];
@@ -649,7 +648,7 @@ __device__ void softmax(const Params& p, const int t, uint32_t sbase, uint32_t t
       }
     }
     if (live && (p.lse || it.slot >= 0)) {
-      const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : NAN);
+      const float lse = l > 0.f ? (m + (log2f(l) - T::kLiftLag)) * kLn2 : (l == 0.f ? -INFINITY : NAN);
       if (it.slot >= 0)
         p.part_l[prow] = lse;
       else
