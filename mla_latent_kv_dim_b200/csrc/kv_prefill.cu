@@ -108,7 +108,7 @@ struct Params {
   int B, T, Hkv, g, gg, groups, tpt;  // gg heads of a row group, tpt tokens of a tile
   int paired;            // the order of the items, see Items
   int causal;
-  float scale_log2;      // |softmax scale| * log2(e) (> 0; see the launcher)
+  float scale_log2;      // |softmax scale| * log2(e), > 0 (see the launcher)
   int negate;            // scale < 0
   const int* count;      // entries of the list (and of joins), or null: one request, no list
   const Entry* list;
@@ -1073,9 +1073,10 @@ cudaError_t launch_kv_prefill(const KvPrefillProblem& dp, void* ws, cudaStream_t
   p.tpt = s.tpt;
   p.causal = dp.causal;
   // The row maximum is taken of the raw scores, negated for a negative scale.
-  // A zero scale becomes 1e-30: every finite score gives exp2(~0) = 1 exactly
-  // in f32, masked (-inf) ones still 0.
-  p.scale_log2 = fmaxf((float)(fabs((double)dp.scale) * 1.4426950408889634), 1e-30f);
+  // A zero scale becomes f32's least number, 2^-149: masked scores (-inf) still
+  // weigh 0, and the largest product there is, 2^128, moves a weight by 2^-21.
+  const float scale_log2 = (float)(fabs((double)dp.scale) * 1.4426950408889634);
+  p.scale_log2 = scale_log2 > 0.f ? scale_log2 : 0x1p-149f;
   p.negate = dp.scale < 0.f;
   p.out = dp.out;
   p.out_dtype = dp.out_dtype;
