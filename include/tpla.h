@@ -445,7 +445,7 @@ TPLA_API int tpla_kv_append(const tpla_tensor* k_new, const tpla_tensor* v_new,
  *   seq_lens  [B] int32, contiguous (0 allowed: out = 0, lse = -inf).
  *   out       [B, Hq, Dv], F32 or q's type, rows on 16-byte boundaries;
  *   lse       [B, Hq, 1] f32 or NULL.
- *   scale     any finite value.
+ *   scale     any value up to 2.3e38 (scale * log2(e) has to be finite).
  *   workspace tpla_kv_decode_workspace_size bytes, 16-byte aligned, or NULL
  *             (cudaMallocAsync / cudaFreeAsync on `stream`).  Calls that may
  *             run at the same time need workspaces of their own.

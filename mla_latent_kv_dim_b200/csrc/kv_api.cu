@@ -199,6 +199,9 @@ int check_results(const tpla_tensor* out, const tpla_tensor* lse, int dtype, int
   return TPLA_OK;
 }
 
+// The kernels work in log2 units: scale log2(e) has to be an f32 too.
+bool check_scale(float scale) { return isfinite((float)(scale * 1.4426950408889634)); }
+
 // Queries [rows, Hq, Dk] against Hkv heads of Dk and Dv columns.
 int check_heads(const tpla_tensor* q, int dtype, int64_t Hkv, int64_t Dk, int64_t Dv) {
   if (!q || q->dtype != dtype || !check_tensor(q, dtype, 3) || !rows16(q) || q->shape[2] != Dk)
@@ -234,7 +237,7 @@ int build_decode(const tpla_tensor* q, const tpla_tensor* k, const tpla_tensor* 
                  const tpla_tensor* seq, const tpla_tensor* pt, float scale,
                  const tpla_tensor* out, const tpla_tensor* lse, KvDecodeProblem* p) {
   memset(p, 0, sizeof(*p));
-  if (!q || !k || !v || !isfinite(scale)) return TPLA_ERR_INVALID_ARG;
+  if (!q || !k || !v || !check_scale(scale)) return TPLA_ERR_INVALID_ARG;
   const int64_t B = q->ndim == 3 ? q->shape[0] : -1;
   if (B > kMaxBatch) return TPLA_ERR_UNSUPPORTED;
   int64_t cap = 0;
@@ -270,7 +273,7 @@ int build_kv_prefill(const tpla_tensor* q, const tpla_tensor* k, const tpla_tens
                      const tpla_tensor* pt, int causal, float scale, const tpla_tensor* out,
                      const tpla_tensor* lse, KvPrefillProblem* p) {
   memset(p, 0, sizeof(*p));
-  if (!q || !k || !v || !isfinite(scale) || !(causal == 0 || causal == 1))
+  if (!q || !k || !v || !check_scale(scale) || !(causal == 0 || causal == 1))
     return TPLA_ERR_INVALID_ARG;
   if (!check_tensor(cu_q, TPLA_I32, 1) || cu_q->shape[0] < 1 ||
       (cu_q->shape[0] > 1 && cu_q->stride[0] != 1))
