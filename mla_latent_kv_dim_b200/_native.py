@@ -381,6 +381,18 @@ def _kv_check(fn: str, rc: int, tensors, workspace=None) -> None:
     _check(fn, rc)
 
 
+_OUT_DT = {t: _DT[t] for t in (torch.bfloat16, torch.float16, torch.float32)}
+
+
+def _out_code(out_dtype, out) -> int:
+    """Type code of the result that a call allocates; ``out`` has its own."""
+    if out is not None:
+        return TPLA_F32
+    if out_dtype not in _OUT_DT:
+        raise TypeError(f"unsupported out_dtype {out_dtype}")
+    return _OUT_DT[out_dtype]
+
+
 def _stream_context(stream):
     """Context in which ``stream`` (a torch stream or a raw handle) is the
     current one, so that what a call allocates belongs to it."""
@@ -429,8 +441,8 @@ def kv_decode(q, k_cache, v_cache, seq_lens, page_table, scale=None, out=None, l
             return kv_decode(q, k_cache, v_cache, seq_lens, page_table, scale, out, lse,
                              workspace=workspace, out_dtype=out_dtype, want_lse=want_lse)
     rc, out_, lse_ = (_bind or _binding()).kv_decode(
-        q, k_cache, v_cache, seq_lens, page_table, out, lse, workspace, scale, _DT[out_dtype],
-        1 if want_lse else 0)
+        q, k_cache, v_cache, seq_lens, page_table, out, lse, workspace, scale,
+        _out_code(out_dtype, out), 1 if want_lse else 0)
     if rc:
         _kv_check("tpla_kv_decode", rc, (q, k_cache, v_cache, seq_lens, page_table, out, lse),
                   workspace)
@@ -456,7 +468,7 @@ def kv_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, seq_lens=None, page_
                               workspace=workspace, out_dtype=out_dtype, want_lse=want_lse)
     rc, out_, lse_ = (_bind or _binding()).kv_prefill(
         q, k, v, cu_seqlens_q, cu_seqlens_k, seq_lens, page_table, out, lse, workspace,
-        1 if causal else 0, scale, _DT[out_dtype], 1 if want_lse else 0)
+        1 if causal else 0, scale, _out_code(out_dtype, out), 1 if want_lse else 0)
     if rc:
         _kv_check("tpla_kv_prefill", rc, (q, k, v, cu_seqlens_q, cu_seqlens_k, seq_lens,
                                           page_table, out, lse), workspace)

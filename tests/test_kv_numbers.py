@@ -24,3 +24,15 @@ def test_scales_that_are_taken(scale):
     assert _decode(scale=scale, ws=0x10000, bytes=16) not in (0, INVALID)
     if not torch.cuda.is_available():
         assert _prefill(scale=scale) == -2
+
+
+@pytest.mark.parametrize("out_dtype", [torch.int32, torch.float64, torch.int8, None])
+def test_output_types(out_dtype):
+    """Refused by name, whatever else is given; not answered with f32."""
+    b = torch.zeros((1, 2, 64), dtype=torch.bfloat16)
+    c = torch.zeros((1, 64, 2, 64), dtype=torch.bfloat16)
+    i = torch.zeros((1,), dtype=torch.int32)
+    with pytest.raises(TypeError, match="out_dtype"):
+        tp.kv_decode(b, c, c, i, i[None], scale=0.1, out_dtype=out_dtype)
+    with pytest.raises(TypeError, match="out_dtype"):
+        tp.kv_prefill(b, b, b, i, scale=0.1, out_dtype=out_dtype)
