@@ -9,6 +9,7 @@ loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -347,22 +348,25 @@ def prefill(q, kv_new, start, page_row, kv_cache, norm_groups=1, hadamard=False,
 
 # ---------------------------------------------------------------- uncompressed keys and values
 _bind = None
-_BINDING_PATH = os.path.join(_PKG, "_kvbind.so")
 
 
 def _binding():
     """The extension that marshals the kv_* calls (csrc/kv_binding.cpp), built
-    in-tree like the library; it calls the library loaded by ``lib``."""
+    in-tree like the library for this Python and torch; it calls the library
+    loaded by ``lib``."""
     global _bind
     if _bind is not None:
         return _bind
     L = lib()
     with _lock:
         if _bind is None:
-            if not os.path.exists(_BINDING_PATH):
-                from . import build as _build
-                _build.build()
-            from . import _kvbind
+            from . import build as _build
+            path = _build.binding_path()
+            if not os.path.exists(path):
+                _build.build_binding()
+            spec = importlib.util.spec_from_file_location(f"{__package__}._kvbind", path)
+            _kvbind = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(_kvbind)
             _kvbind.init(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
                 "tpla_kv_append", "tpla_kv_decode_workspace_size", "tpla_kv_decode",
                 "tpla_kv_prefill_workspace_size", "tpla_kv_prefill")))

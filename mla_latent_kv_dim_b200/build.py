@@ -1,5 +1,9 @@
-"""Build libtpla.so in-tree with nvcc for sm_100a, and the Python extension
-_kvbind.so beside it.
+"""Build libtpla.so in-tree with nvcc for sm_100a, and beside it the Python
+extension that marshals the tpla_kv_* calls.
+
+The library is C and needs nvcc alone.  The extension needs torch with CUDA,
+g++ and Python's headers, and belongs to the Python and torch it was built
+with: both are in its name, so that others look for one of their own.
 
 Usage: python -m mla_latent_kv_dim_b200.build [--force]
 """
@@ -9,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -16,7 +21,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtpla.so")
-BINDING = os.path.join(PKG, "_kvbind.so")
 SOURCES = ["api.cu", "decode_generic.cu", "decode_sm100.cu", "merge.cu", "hadamard.cu",
            "vup.cu", "noalloc.cu", "pca.cu", "append.cu", "kv_api.cu", "kv_append.cu", "kv_decode.cu",
            "kv_prefill.cu"]
@@ -43,11 +47,16 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _binding_command() -> list[str]:
-    """g++ command of the Python extension that marshals the tpla_kv_* calls
-    (torch's headers and libraries; no CUDA code)."""
-    import sysconfig
+def binding_path() -> str:
+    """The extension of this Python and torch."""
+    import torch
+    return os.path.join(PKG, f"_kvbind.torch-{torch.__version__}"
+                             f"{sysconfig.get_config_var('EXT_SUFFIX')}")
 
+
+def _binding_command(target: str) -> list[str]:
+    """g++ command of the extension (torch's headers and libraries; no CUDA
+    code)."""
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
@@ -57,11 +66,20 @@ def _binding_command() -> list[str]:
             "-isystem", os.path.join(base, "include"),
             "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
             "-isystem", os.path.join(cuda, "include"),
-            os.path.join(CSRC, "kv_binding.cpp"), "-o", BINDING,
+            os.path.join(CSRC, "kv_binding.cpp"), "-o", target,
             "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
+def _run(cmd: list[str], verbose: bool) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compiler failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout + r.stderr)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    """The library; returns its path."""
     os.makedirs(OBJ, exist_ok=True)
     nvcc = _nvcc()
     headers = [os.path.join(ROOT, "include", "tpla.h")] + [
@@ -74,24 +92,40 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(o)
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, *_flags(), "-c", s, "-o", o])
-    compiled = bool(jobs)
-    if force or _stale(BINDING, [os.path.join(CSRC, "kv_binding.cpp"), headers[0]]):
-        jobs.append(_binding_command())
-
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("compiler failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout + r.stderr)
-
     with ThreadPoolExecutor(max_workers=min(8, max(1, len(jobs)))) as ex:
-        list(ex.map(run, jobs))
-    if force or compiled or _stale(LIB, objs):
-        run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", LIB, *objs,
-             "-Xlinker", "--no-undefined", "-ldl"])
+        list(ex.map(lambda cmd: _run(cmd, verbose), jobs))
+    if force or jobs or _stale(LIB, objs):
+        _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", LIB, *objs,
+              "-Xlinker", "--no-undefined", "-ldl"], verbose)
     return LIB
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The extension; returns its path."""
+    target = binding_path()
+    if force or _stale(target, [os.path.join(CSRC, "kv_binding.cpp"),
+                                os.path.join(ROOT, "include", "tpla.h")]):
+        # under another name until it is whole: other processes may look for it
+        part = f"{target}.{os.getpid()}"
+        try:
+            _run(_binding_command(part), verbose)
+            os.replace(part, target)
+        finally:
+            if os.path.exists(part):
+                os.remove(part)
+    return target
+
+
+def main() -> int:
+    force = "--force" in sys.argv
+    print(build(force=force, verbose=True))
+    try:
+        print(build_binding(force=force, verbose=True))
+    except (ImportError, OSError, RuntimeError) as e:
+        print(f"The library is built. Python's kv_append, kv_decode and kv_prefill need an "
+              f"extension that could not be built here:\n{e}", file=sys.stderr)
+    return 0
+
+
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose=True))
+    sys.exit(main())
