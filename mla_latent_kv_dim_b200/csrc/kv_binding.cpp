@@ -14,6 +14,7 @@
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "tpla.h"
@@ -125,12 +126,13 @@ bool get_workspace(PyObject* o, int* device, Arg* a, int* bad) {
   return true;
 }
 
+// What torch raises (an allocation that does not fit, say) stays its own error.
 #define KV_TRY try {
-#define KV_CATCH                                       \
-  }                                                    \
-  catch (const std::exception& e) {                    \
-    PyErr_SetString(PyExc_RuntimeError, e.what());     \
-    return nullptr;                                    \
+#define KV_CATCH                                                  \
+  }                                                               \
+  catch (...) {                                                   \
+    torch::translate_exception_to_python(std::current_exception()); \
+    return nullptr;                                               \
   }
 
 PyObject* py_init(PyObject*, PyObject* const* a, Py_ssize_t n) {
