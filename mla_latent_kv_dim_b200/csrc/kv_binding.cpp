@@ -168,7 +168,9 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (bad == 0 && !t[8].none && t[9].none && !t[5].none)
     make(&t[9], t[8].t.sizes(), t[8].t, t[5].t.scalar_type());
   int rc = bad;
-  if (bad == 0)
+  if (bad == 0 && (off != (int)off || q_off != (int)q_off))
+    rc = TPLA_ERR_INVALID_ARG;  // no column, and not one modulo 2^32
+  else if (bad == 0)
     rc = g_append(t[0].ptr(), t[1].ptr(), t[2].ptr(), t[3].ptr(), t[4].ptr(), t[5].ptr(),
                   t[6].ptr(), t[7].ptr(), (int)off, (int)inter, t[8].ptr(), t[9].ptr(), (int)q_off,
                   stream_of(dev));
