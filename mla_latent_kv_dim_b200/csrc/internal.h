@@ -152,6 +152,7 @@ struct KvDecodeProblem {
   float* lse;                   // [B, Hq, 1] or null
   int64_t l_sb, l_sh;
 };
+int sm_count(int device);      // SMs of the device the kv calls run on
 bool kv_head_dims_supported(int Dk, int Dv);
 size_t kv_decode_workspace_bytes(const KvDecodeProblem& p, int device);
 cudaError_t launch_kv_decode(const KvDecodeProblem& p, void* ws, cudaStream_t stream);

@@ -359,6 +359,17 @@ int with_workspace(void* ws, size_t have, size_t need, cudaStream_t s, F launch)
 }
 
 }  // namespace
+
+int sm_count(int device) {
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+      sms < 1) {
+    cudaGetLastError();
+    sms = 148;  // no device: the workspace sizes of a B200
+  }
+  return sms;
+}
+
 }  // namespace tpla
 
 using namespace tpla;

@@ -212,7 +212,7 @@ template <typename T, bool KVF32, bool QF32, bool INTER>
 void launch_form(const KvAppendProblem& p, int slices, cudaStream_t stream) {
   // Many tokens a block once that still gives every SM the blocks it can hold,
   // else one: the latency counts.
-  if ((int64_t)p.T * slices >= 148 * 8 * kTokens)
+  if ((int64_t)p.T * slices >= (int64_t)sm_count(current_device()) * 8 * kTokens)
     kv_append_kernel<T, kTokens, KVF32, QF32, INTER>
         <<<dim3((p.T + kTokens - 1) / kTokens, slices), kThreads, 0, stream>>>(p);
   else

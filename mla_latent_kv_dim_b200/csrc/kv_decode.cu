@@ -707,12 +707,7 @@ Schedule schedule(const KvDecodeProblem& p, int device) {
   s.g = p.Hq / p.kv.Hkv;
   s.groups = (s.g + kMaxRows - 1) / kMaxRows;
   s.rows = s.g < kMaxRows ? s.g : kMaxRows;
-  int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-      sms < 1) {
-    cudaGetLastError();
-    sms = 148;
-  }
+  const int sms = sm_count(device);
   const int64_t pages = (p.kv.cap_rows + kPage - 1) / kPage;
   const int64_t units = (pages + kSegUnits) * p.B * p.kv.Hkv * s.groups;
   const int most = s.rows <= 16 ? 2 * sms : sms;

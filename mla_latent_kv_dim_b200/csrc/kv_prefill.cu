@@ -970,16 +970,6 @@ Shape shape(const KvPrefillProblem& p, int sms) {
   return s;
 }
 
-int sm_count(int device) {
-  int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-      sms < 1) {
-    cudaGetLastError();
-    sms = 148;
-  }
-  return sms;
-}
-
 template <typename T, int DK, int DV>
 cudaError_t launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
                    const Params& p, int slots, int grid, int dev, cudaStream_t stream) {
