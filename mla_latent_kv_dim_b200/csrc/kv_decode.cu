@@ -318,7 +318,8 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   uint32_t n = 0;  // stages so far
 
   if (produces) {  // ------------------------------------------------------- producer
-    while (seg_next(p, range, w, s)) {
+    int ok = 1;
+    while (ok && seg_next(p, range, w, s)) {
       const int hk = s.task / p.groups;
       int win = 0;  // lane i: page id of page w0 + i
       for (int pg = s.page0, w0 = pg; pg < s.page1; ++pg, ++n) {
@@ -328,11 +329,11 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         }
         const int blk = p.page_table ? __shfl_sync(0xffffffffu, win, pg - w0) : s.b;
         const int slot = n % C::kStages;
-        int ok = 1;
         if (lane == 0 && n >= C::kStages)
           ok = wait_bar(smem_addr(&ms.empty[slot]), ((n / C::kStages) - 1) & 1, abort_flag,
                         &g_kv_decode_status);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
         if (lane == 0) {
           const int row = p.page_table ? 0 : pg * kPage;
           const uint32_t full = smem_addr(&ms.full[slot]);
@@ -350,6 +351,11 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         }
         __syncwarp();
       }
+    }
+    if (lane == 0) {  // no copy outlives the block, whatever its consumers do
+      const long long since = clock64();
+      for (uint32_t i = n < C::kStages ? 0 : n - C::kStages; i < n; ++i)
+        wait_landed(smem_addr(&ms.full[i % C::kStages]), (i / C::kStages) & 1, since);
     }
     return;
   }

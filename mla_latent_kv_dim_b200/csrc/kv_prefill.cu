@@ -291,10 +291,11 @@ __device__ void producer(const Params& p, const CUtensorMap* km, const CUtensorM
   Items items(p);
   Item it;
   uint32_t slot = 0, phase = 1;
-  uint32_t tile = 0;
-  while (items.next(p, it)) {
+  uint32_t tile = 0, sent[2] = {0, 0};  // K and V tiles under way or landed
+  int ok = 1;
+  while (ok && items.next(p, it)) {
     int win = 0;  // lane i: the page id of key tile 32 w + i
-    for (int j = 0; j < it.nmax; ++j, ++tile) {
+    for (int j = 0; ok && j < it.nmax; ++j, ++tile) {
       int page = 0, row = it.e.k0 + kKeys * (it.e.j0 + j), flag = 0;
       if (p.page_table) {
         if ((j & 31) == 0)
@@ -312,7 +313,6 @@ __device__ void producer(const Params& p, const CUtensorMap* km, const CUtensorM
       for (int v = 0; v < 2; ++v) {
         constexpr int kN[2] = {C::kNK, C::kNV};
         const uint32_t full = smem_addr(&ms.full[slot][v]);
-        int ok = 1;
         if (lane == 0) {
           if (tile >= C::kRing)
             ok = wait_bar(smem_addr(&ms.empty[slot][v]), phase, abort_flag, &g_kv_prefill_status);
@@ -324,7 +324,9 @@ __device__ void producer(const Params& p, const CUtensorMap* km, const CUtensorM
             mbar_arrive_expect_tx(full, kN[v] * kChunk);
           }
         }
-        if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        sent[v] = tile + 1;
         const int c = lane - (v ? C::kNK : 0);
         if (c >= 0 && c < kN[v])
           tma_load_5d(sbase + 2 * C::kQTile + slot * C::kKV + lane * kChunk, v ? vm : km, 0, row, c,
@@ -335,6 +337,12 @@ __device__ void producer(const Params& p, const CUtensorMap* km, const CUtensorM
         phase ^= 1;
       }
     }
+  }
+  if (lane < 2) {  // no copy outlives the block, whatever the other roles do
+    const long long since = clock64();
+    const uint32_t n = lane ? sent[1] : sent[0];
+    for (uint32_t i = n < C::kRing ? 0 : n - C::kRing; i < n; ++i)
+      wait_landed(smem_addr(&ms.full[i % C::kRing][lane]), (i / C::kRing) & 1, since);
   }
 }
 
@@ -374,6 +382,7 @@ __device__ void qk_issuer(const Params& p, const int t, const CUtensorMap* qm, u
     __syncwarp();
     if (lane == 0) {
       ok = wait(q_full, i & 1);
+      if (!ok) wait_landed(q_full, i & 1, clock64());
       for (int j = 0; ok && j < n; ++j, ++cnt) {
         const uint32_t buf = cnt & 1;
         ok = wait(smem_addr(&ms.full[slot][0]), phase) &&

@@ -54,6 +54,14 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   }
 }
 
+// Bounded wait of a thread whose own copies may still be on their way into the
+// CTA's shared memory when it ends (another wait gave up): the abort flag does
+// not shorten it.
+__device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity, long long since) {
+  while (!mbar_try_wait_sleep(bar, parity, kWaitSleepNs))
+    if (clock64() - since > kTimeoutCycles) return;
+}
+
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
