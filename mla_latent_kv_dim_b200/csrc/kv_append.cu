@@ -16,11 +16,12 @@
 // of position, request and page is followed once a token, by one thread, while
 // the others' first values are on their way.
 //
-// Measured (B200): sixteen prompts, 11900 tokens of 8 + 8 heads of 128 and 64
-// queries, f32 in and f16 out, 733 MB: 139 us, 5.3 TB/s, 81 % of a copy's rate;
-// 4096 latent rows with the rope columns of 128 heads' queries, 144 MB: 32 us,
-// 69 %; one token of 64 requests: 2.7 us, a launch and the chain of position,
-// page and row.
+// Measured (B200, the public Python call on data that the L2 does not hold):
+// sixteen prompts, 11900 tokens of 8 + 8 heads of 128 and 64 queries, f32 in and
+// f16 out, 733 MB: 141 us, 5.2 TB/s, 80 % of a copy's rate; 4096 latent rows with
+// the rope columns of 128 heads' queries, 144 MB: 33.5 us, 66 % (one wave of
+// blocks, one token ahead, 72 of a key block's 128 threads in use); one token of
+// 64 requests: 4.1 us, a launch and the chain of position, page and row.
 #include <stdint.h>
 
 #include "internal.h"
@@ -35,7 +36,7 @@ __device__ int g_kv_append_status;
 
 constexpr int kThreads = 128;
 // Tokens of a block in a large call; 4, 8, 16, 32: 155, 144, 140, 142 us for the
-// sixteen prompts above (256 threads: 154)
+// sixteen prompts above in a replayed graph (256 threads: 154)
 constexpr int kTokens = 16;
 
 // 8 consecutive values as they stand in memory: 16 or 32 bytes

@@ -14,20 +14,26 @@
 // A block is eight consumer warps and TMA producer warps over rings of
 // 64-token stages (K and V of one page of one key head, 128-byte swizzle).
 // The g query heads are the rows of one or more 16-row matrix products
-// (mma.sync m16n8k16: a page gives the tensor core too little work to gain
-// from TMEM accumulators; the copies are the limit).  Warps split rows (16
+// (mma.sync m16n8k16: up to 16 rows a page gives the tensor core too little
+// work to gain from TMEM accumulators, and the copies are the limit; with more
+// rows every 16 of them read the page from shared memory again, see the figures
+// for g > 16 below).  Warps split rows (16
 // each, for g > 16) and then tokens; each keeps its own running maximum, sums
 // and accumulator in registers, so nothing in the loop waits for another
 // warp, and they meet once at the end of a (request, head) segment.  Up to 16
 // rows the consumers are two groups of four warps, each with its slice, its
 // ring and its producer: one group's segment end passes while the other reads.
 //
-// Measured (B200, bytes of the cache against a copy's 6542 GB/s): 4 requests of
-// 131072 tokens, 64 heads over 8 of 128: 317 us, 6.8 TB/s, 104 %; 32 of 2048 to
-// 4096, 32 over 8: 74 us, 86 %; 13 ragged ones of 16 heads, 192 / 128, f16: 70
-// us, 79 % (the slices' ends: start, last page, joins, merge); 1 of 256 tokens:
-// 8.6 us, nearly all fixed (start 2, one page 2.5, join 0.7, merge launch and
-// read 1.5).
+// Measured (B200, the public Python call on data that the L2 does not hold;
+// bytes of the cache against a copy's 6542 GB/s): 4 requests of 131072 tokens, 64
+// heads over 8 of 128: 321 us, 6.7 TB/s, 102 %; 32 of 2048 to 4096, 32 over 8: 76
+// us, 83 %; 13 ragged ones of 16 heads, 192 / 128, f16: 72 us, 76 % (the slices'
+// ends: start, last page, joins, merge); 1 of 256 tokens: 10.3 us, nearly all
+// fixed (in a replayed graph 8.6: start 2, one page 2.5, join 0.7, merge launch
+// and read 1.5).  32 requests of 2048 to 4063 tokens, 8 key heads of 128, by g: 1:
+// 73 us; 4: 74; 16: 77; 17: 97; 32: 99; 33: 152; 64: 157; 65: 361; 128: 368 (192 /
+// 128: 95, 96, 100, 119, 122, 174, 183, 308, 320).  From 17 rows on the copies (61
+// and 77 us) bound it no longer.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -48,7 +54,8 @@ constexpr int kPage = 64;
 constexpr int kConsumers = 8;                      // warps
 constexpr int kMaxRows = 128;                      // query heads of one row group
 constexpr int kMaxStages = 12;
-constexpr int kSegUnits = 3;  // 13 ragged requests of 16 heads: 94, 87, 71, 68, 68 us for 0 to 4
+// 13 ragged requests of 16 heads in a replayed graph: 94, 87, 71, 68, 68 us for 0 to 4
+constexpr int kSegUnits = 3;
 constexpr int kSmemMax = 232448;
 constexpr int kMiscBytes = 2560;                   // barriers, stage counts, statistics
 

@@ -33,12 +33,15 @@
 //    kernel cuts their keys into pieces, whose normalised results a third
 //    kernel joins by their log-sum-exp.
 //
-// Measured (B200 at 1.97 GHz, bf16 in and out; of the burst rate of a library
-// product, 1651 TFLOP/s): 16384 tokens of 8 heads over one of 128: 451 us, 1218
-// TFLOP/s, 74 %; 128 heads of 4096 tokens, 192 / 128 wide: 648 us, 64 %; chunks
-// of four prompts after 4000 to 8000 tokens (f16, paged): 177 us, 57 %; twelve
-// prompts of 33 to 1500 tokens: 86 us, 39 %; one of 77 tokens: 7.6 us, mostly
-// fixed (an empty kernel takes 1 us, the start 2, a chain of two key tiles 3).
+// Measured (B200, the public Python call on data that the L2 does not hold, bf16
+// in and out; of the burst rate of a library product, 1651 TFLOP/s): 16384 tokens
+// of 8 heads over one of 128: 527 us, 1040 TFLOP/s, 63 %; 128 heads of 4096
+// tokens, 192 / 128 wide: 752 us, 55 %; chunks of four prompts after 4000 to 8000
+// tokens (f16, paged): 208 us, 48 %; twelve prompts of 33 to 1500 tokens: 96 us,
+// 35 %; one of 77 tokens: 9.4 us, mostly fixed (an empty kernel takes 1 us, the
+// start 2, a chain of two key tiles 3).  Replayed graphs, which find their data
+// in the L2 and were taken at 1.97 GHz, take 451, 648, 177, 86 and 7.6 us.
+//
 // What bounds it is feeding the tensor core: of 1750 cycles a step of 64 keys at
 // Dk = 128 its pipe is taken 82 % of the time (1430 cycles, 1024 of them at the
 // full rate), the exponential unit 44 %, the schedulers 53 %; beyond that the two
@@ -77,9 +80,9 @@ constexpr uint32_t kColS = 0, kColO = 256;
 
 // One pair of weights in this many comes from the FMA pipe instead of the
 // exponential unit, which both warpgroups wait for at the same time.  None, one
-// in 8, 4, 3: chunk of four prompts 200, 194, 184, 185 us; packed 91, 87, 84, 85.
-// Not where Dk is 192: there Q K^T takes longer than the exponentials (128
-// heads of 4096 tokens 695 us without, 708 with).
+// in 8, 4, 3, replayed: chunk of four prompts 200, 194, 184, 185 us; packed 91,
+// 87, 84, 85.  Not where Dk is 192: there Q K^T takes longer than the exponentials
+// (128 heads of 4096 tokens, replayed: 695 us without, 708 with).
 constexpr int kFmaEvery = 4;
 constexpr int64_t kL2Share = 96 << 20;  // bytes of keys and values that the L2 keeps
 constexpr int kMinPiece = 8;  // key tiles; a shorter piece is mostly fixed work
@@ -860,7 +863,7 @@ __global__ void __launch_bounds__(1024) kv_prefill_plan_kernel(const Params p, E
 // Joins the pieces of an item,
 //   lse = ln sum_i exp(lse_i),  out = sum_i exp(lse_i - lse) out_i:
 // a thread per row and 16 columns, the rows of a warp side by side.  (8 columns
-// and a quarter of the blocks: chunk of four prompts 187 us, now 179.)
+// and a quarter of the blocks: chunk of four prompts 187 us, replayed, now 179.)
 constexpr int kJoinThreads = 128, kJoinColumns = 16;
 
 template <int DV>
@@ -966,7 +969,8 @@ Shape shape(const KvPrefillProblem& p, int sms) {
   // use at once.  Where the L2 (126 MB) does not keep those, the items of one
   // prompt go head after head in pairs; the last round of pairs must be nearly
   // full, because a pair is up to twice an item.  128 heads of 4096 tokens
-  // (335 MB of keys and values): 728 us longest first, 648 in pairs.
+  // (335 MB of keys and values), replayed: 728 us longest first, 648 in pairs.
+  // Calls of several prompts keep the longest-first order.
   const int64_t pairs = ((s.entries - p.B + 1) / 2) * s.heads, rounds = (pairs + sms - 1) / sms;
   s.paired = !s.planned && pairs > 0 && rounds * sms <= pairs + pairs / 16 &&
              p.kv.cap_rows * (p.kv.Dk + p.kv.Dv) * 2 * p.kv.Hkv > kL2Share;

@@ -152,8 +152,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // 2^y of two values below 2^7 without the exponential unit: y = n + f with n
 // the nearest integer (it appears in the low bits of y + 1.5 2^23), the
 // polynomial of degree 5 with the least greatest relative error of 2^f on
-// [-1/2, 1/2] (found by exchange, 7.5e-8; 2.2e-7 with the f32 roundings,
-// measured over [-126, 8]), times 2^n put together from its bits.  At y <= -127,
+// [-1/2, 1/2] (found by exchange: 7.5e-8, with its coefficients rounded to f32
+// 1.55e-7; 2.2e-7 in f32 arithmetic, measured over [-126, 8]), times 2^n put together from its bits.  At y <= -127,
 // -inf included, 2^n is 0 and so is the result; NaN stays NaN.
 __device__ __forceinline__ void f2_ex2_fma(uint64_t y, float& e0, float& e1) {
   float a, b;
@@ -189,8 +189,9 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
 // the largest at 2^15.  The sums carry the same factor, which the division
 // takes out.  Prefill lets weights grow to 2^kLag before it rescales, and
 // lifts them by that much less (kLiftLag): below 2^-34 of the largest they
-// count as 0.  (Four prompts' chunks after 4000 to 8000 tokens, fp16: 209 us
-// with a kLag of 8 or 6, 221 with 4, which rescales more often.)
+// count as 0.  (Four prompts' chunks after 4000 to 8000 tokens, fp16, through
+// the public call: 209 us with a kLag of 8 or 6, 221 with 4, which rescales
+// more often.)
 struct Bf16 {
   using type = __nv_bfloat16;
   static constexpr float kLift = 0.f, kLag = 8.f, kLiftLag = 0.f;
