@@ -80,3 +80,31 @@ def test_decode_over_a_dominant_first_token(cuda_dev, Hq):
     out, lse = tp.kv_decode(q, k, v, n, pt, scale=0.125)
     _check(out, lse, L, DECODE)
     assert tp.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,step", [(torch.float16, 5.9), (torch.float16, 6.1),
+                                        (torch.bfloat16, 7.9), (torch.bfloat16, 8.1)])
+def test_maxima_that_climb_by_nearly_the_lag(cuda_dev, dtype, step):
+    """Scores that climb by `step` log2 units from a key tile of 64 to the next,
+    just below and above what prefill lets weights grow by before it rescales:
+    none overflows, and the last tile, which has nearly all of the weight, gives
+    the result.  Tile j's scores are all s_j (k is s_j in one column and 0 in
+    the others, q 1, the scale 1), its values j: out is a mean of whole numbers."""
+    tiles = 12
+    s = (torch.arange(tiles) * step * math.log(2)).to(dtype)
+    k = torch.zeros((64 * tiles, 1, 64), dtype=dtype)
+    k[:, 0, 0] = s.repeat_interleave(64)
+    v = torch.arange(tiles).repeat_interleave(64).to(dtype)[:, None, None].expand(-1, 1, 64).contiguous()
+    q = torch.zeros((256, 1, 64), dtype=dtype)
+    q[..., 0] = 1
+    cq = torch.tensor([0, 256], dtype=torch.int32, device=cuda_dev)
+    ck = torch.tensor([0, 64 * tiles], dtype=torch.int32, device=cuda_dev)
+    out, lse = tp.kv_prefill(q.to(cuda_dev), k.to(cuda_dev), v.to(cuda_dev), cq, ck, scale=1.0,
+                             causal=False)
+    p = torch.softmax(s.double(), 0)
+    want, want_lse = (p * torch.arange(tiles)).sum().item(), torch.logsumexp(s.double(), 0).item() + math.log(64)
+    # one rounding a weight; arguments below 2^7 log2 units in f32: 2^-17 of a weight
+    eps = torch.finfo(dtype).eps / 2
+    error, lse_error = (out.double() - want).abs().max().item(), (lse.double() - want_lse).abs().max().item()
+    assert error <= (eps + 2.0 ** -16) * want and lse_error <= 2.0 ** -16
+    assert tp.device_status() == 0
